@@ -94,6 +94,7 @@ typedef int csa2_status;
 #define CSA2_DEV_FP16_RANGE 4u     /* an attention operand lies outside the fp16-exact range; output invalid */
 #define CSA2_DEV_LENGTH 8u         /* a device length exceeded the host bound (max_len / n_entries); clamped */
 #define CSA2_DEV_TIMEOUT 16u       /* a pipeline wait inside a kernel gave up after its time limit; output invalid */
+#define CSA2_DEV_NO_TOKEN 32u      /* a distribution to draw from held no positive probability; token -1 */
 
 /* One MXFP4 cache (main KV: n = 512, indexer K: n = 128).  `rows` is the
  * capacity in rows (multiple of 8).  Pointers must be 16-byte aligned. */
@@ -461,6 +462,157 @@ csa2_status csa2_sparse_attn_decode_noalloc(const uint16_t* q, csa2_mxfp4_cache 
                                             const int32_t* seq_len, const int32_t* topk, int k, const uint8_t* win,
                                             const float* win_scale, const int32_t* win_len, float sm_scale,
                                             float* out, float* lse, uint32_t* flags_out, int B, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * csa2_verify_drafts -- which candidates of a verification step stand, and
+ * the next token of every sequence.
+ * Source: [V41] section "DSpark" (several draft positions per request, the
+ * ones that the target model confirms are kept); the pages do not print the
+ * rule.  It is the usual speculative sampling, whose outcome is distributed
+ * as if every token were drawn from the target alone.
+ * Sequence b owns candidates q_off[b] .. q_off[b+1]-1 (n of them, as in
+ * csa2_index_multi): candidate 0 is its last known token, the others are
+ * drafts.  With i counted inside the sequence, row i of `target` is the
+ * target's distribution p_i of the token behind candidate i, and row i of
+ * `draft` the distribution q_i from which candidate i+1 was drawn (the row of
+ * the last candidate is not read).
+ *   accept:  for i = 0, 1, .. candidate i+1 (token x) stands iff
+ *            u_i * q_i(x) < p_i(x); the first that does not ends the prefix.
+ *            n_accept[b] = how many stand (0 .. n-1).
+ *   next:    a = n_accept[b]; w = max(p_a - q_a, 0) where a draft was
+ *            rejected (or p_a where that is zero everywhere), w = p_a behind
+ *            the last candidate; next_tok[b] = the first j with
+ *            w_0 + .. + w_j > r[b] * sum(w).  Products and sums in double.
+ * Without `draft` the drafts were chosen deterministically: q_i is 1 at
+ * candidate i+1's token and 0 elsewhere.
+ * A probability that is negative or NaN counts as 0; rows need not sum to 1
+ * (p and q of one row should have the same sum).  If a row to draw from holds
+ * no positive probability, next_tok[b] = -1 and CSA2_DEV_NO_TOKEN is set.  A
+ * drafted token outside [0, V) is rejected (CSA2_DEV_INDEX_RANGE).  A
+ * sequence without candidates gets n_accept 0 and next_tok -1; offsets that
+ * do not ascend within [0, Q] count as none (CSA2_DEV_LENGTH).
+ *   target     [Q] rows of V probabilities, target_type CSA2_TYPE_*, rows
+ *              target_stride elements apart (any stride >= 0, any alignment
+ *              of the element type)
+ *   draft      the same with its own type and stride, or NULL
+ *   tokens     [Q] int32 token of every candidate;  q_off [B+1] int32
+ *   u          [Q] fp32 random numbers of the tests in [0, 1) (u_i of row i)
+ *   r          [B] fp32 random numbers of the draws in [0, 1)
+ *   seq_len_in, seq_len_out  [B] int32 or both NULL: the cache lengths with
+ *              all n candidates appended, and without the rejected ones
+ *              (seq_len_in - (n - 1 - n_accept)); may be the same array.
+ *              The entries behind them are overwritten by the next append
+ *   n_accept [B], next_tok [B] int32
+ *   out_tokens [B][out_stride] int32 or NULL: the accepted tokens, then the
+ *              next token, then -1 (a next token that does not fit sets
+ *              CSA2_DEV_LENGTH)
+ *   workspace  csa2_verify_drafts_workspace_bytes(B, V)
+ * ------------------------------------------------------------------------- */
+#define CSA2_TYPE_F32 0
+#define CSA2_TYPE_BF16 1
+#define CSA2_TYPE_F16 2
+size_t csa2_verify_drafts_workspace_bytes(int B, int V);
+csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t target_stride, const void* draft,
+                               int draft_type, int64_t draft_stride, const int32_t* tokens, const int32_t* q_off,
+                               const float* u, const float* r, int B, int Q, int V, const int32_t* seq_len_in,
+                               int32_t* seq_len_out, int32_t* n_accept, int32_t* next_tok, int32_t* out_tokens,
+                               int out_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * csa2_attn_weights, csa2_attn_weights_paged -- the attention weight that a
+ * step gave its selected entries, added to the entries' accumulators.
+ * Source: the weights are those of the softmax of csa2_sparse_attn_decode
+ * ([V41] section "三个方向一起压小缓存"); accumulating them has no counterpart
+ * on the pages, it is the ranking that csa2_cache_evict evicts by.
+ * For every query i that counts and every slot j of its selection:
+ *   weights_out[i][j] = sum_h exp(sm_scale * (q_ih . key_j) - lse[i][h])
+ *   acc[row of topk[i][j]] += weights_out[i][j]
+ * with key_j the dequantised main row as in csa2_sparse_attn_decode and lse
+ * its output (window rows included, so a query's weights sum to at most 16).
+ * Empty slots (-1), queries that do not count and heads with lse = -inf give
+ * weight 0, and a weight below 2^-126 (the smallest normal fp32) is 0.  The queries of a sequence are added in their order (results do
+ * not change from run to run); a position listed twice is added twice.
+ *   q          [Q][16][512] bf16;  topk [Q][k] int32;  lse [Q][16] fp32
+ *   seq_row_off [B] int64, seq_len [B] int32: the sequences' rows in main_kv
+ *              (positions >= seq_len[b] are skipped, CSA2_DEV_INDEX_RANGE)
+ *   q_off      [B+1] int32: sequence b owns queries q_off[b] .. q_off[b+1]-1
+ *              (ascending within [0, Q]; others set CSA2_DEV_LENGTH and their
+ *              sequence is not accumulated), or NULL: one query per sequence
+ *              (Q == B)
+ *   n_accept   [B] int32 or NULL (needs q_off): only the first n_accept[b] + 1
+ *              queries of a sequence count, the ones that csa2_verify_drafts
+ *              let stand (NULL: all; a negative number counts as 0)
+ *   acc        [main_kv.rows] fp32, one accumulator per cache row, read and
+ *              written.  The accumulator of a new entry starts at zero: keep
+ *              it zero behind the sequences' ends
+ *   weights_out [Q][k] fp32 or NULL
+ *   workspace  csa2_attn_weights_workspace_bytes(B, Q, k)
+ * Accuracy: relative error of a weight <= 6e-6 * (1 + A), A the largest
+ * sm_scale * sum_d |q_d key_d| of its heads (fp32 sums; bf16 queries and E2M1
+ * codes enter exactly, but elements below 2^-39 of a query row's largest are
+ * rounded).  k is 1..2048.
+ * In the paged call a page id outside the cache sets CSA2_DEV_ROW_LAYOUT and
+ * its entries are skipped.
+ * ------------------------------------------------------------------------- */
+size_t csa2_attn_weights_workspace_bytes(int B, int Q, int k);
+csa2_status csa2_attn_weights(const uint16_t* q, csa2_mxfp4_cache main_kv, const int64_t* seq_row_off,
+                              const int32_t* seq_len, const int32_t* q_off, const int32_t* n_accept,
+                              const int32_t* topk, int k, const float* lse, float sm_scale, float* acc,
+                              float* weights_out, int B, int Q, void* workspace, size_t workspace_bytes,
+                              void* stream);
+csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv, const int32_t* pages, int page_rows,
+                                    int max_pages, const int32_t* seq_len, const int32_t* q_off,
+                                    const int32_t* n_accept, const int32_t* topk, int k, const float* lse,
+                                    float sm_scale, float* acc, float* weights_out, int B, int Q, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * csa2_cache_evict, csa2_cache_evict_paged -- keeps the entries of a cache
+ * that carried the most attention weight, and moves them together.
+ * Source: the pages have no counterpart of eviction (their caches only grow);
+ * the rows moved are the main KV and indexer K of [V41] section
+ * "三个方向一起压小缓存".
+ * Of the L = seq_len[b] entries of sequence b, n = min(keep[b], L) stay: the
+ * last min(last, n), the first min(first, what is left of n), and of the
+ * entries between them the best by (acc descending, position ascending; NaN
+ * ranks below every number).  Kept entries keep their order: kept_out[b][j]
+ * is the source position of the destination's entry j.  Rows of the main
+ * cache, the indexer cache and the accumulators are copied to the destination
+ * rows of positions 0 .. n-1; no other destination byte is written (zero the
+ * accumulators' destination once: new entries' accumulators start at zero).
+ * Positions held from before (pools, selections) refer to the source.
+ *   main_src, main_dst  main-KV caches;  idx_src, idx_dst  indexer-K caches,
+ *              or both with codes and scales NULL
+ *   acc_src    [src rows] fp32;  acc_dst [dst rows] fp32
+ *   src_row_off, dst_row_off  [B] int64 (multiples of 8);  seq_len [B] int32
+ *   keep       [B] int32 entries to keep (negative: 0)
+ *   kept_out   [B][max_keep] int32, -1 padded;  seq_len_out [B] int32 = n (may
+ *              be seq_len itself)
+ *   max_len    host: upper bound of seq_len;  max_keep host, >= 1: upper bound
+ *              of n (larger ones are cut to it, CSA2_DEV_LENGTH)
+ *   first, last  host, >= 0
+ *   workspace  csa2_cache_evict_workspace_bytes(B, max_len)
+ * The destination is other memory than the source: the contiguous call
+ * refuses caches whose memory overlaps; in the paged call the caches may be
+ * the same pool (and pages the two page tables of one pool), but no page of
+ * `dst_pages` may be one that `pages` names for an entry of any sequence.  A
+ * sequence that does not fit its destination is left out (n = 0,
+ * CSA2_DEV_ROW_LAYOUT); rows whose destination page id lies outside the cache
+ * are not written (the same flag).
+ * ------------------------------------------------------------------------- */
+size_t csa2_cache_evict_workspace_bytes(int B, int max_len);
+csa2_status csa2_cache_evict(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
+                             const int64_t* src_row_off, const int32_t* seq_len, const int32_t* keep,
+                             csa2_mxfp4_cache main_dst, csa2_mxfp4_cache idx_dst, float* acc_dst,
+                             const int64_t* dst_row_off, int32_t* kept_out, int32_t* seq_len_out, int B, int max_len,
+                             int max_keep, int first, int last, void* workspace, size_t workspace_bytes,
+                             void* stream);
+csa2_status csa2_cache_evict_paged(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
+                                   const int32_t* pages, int max_pages, const int32_t* seq_len, const int32_t* keep,
+                                   csa2_mxfp4_cache main_dst, csa2_mxfp4_cache idx_dst, float* acc_dst,
+                                   const int32_t* dst_pages, int dst_max_pages, int page_rows, int32_t* kept_out,
+                                   int32_t* seq_len_out, int B, int max_len, int max_keep, int first, int last,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, returns the status word of `workspace` in *flags
  * (CSA2_DEV_* bits) and clears it.  Returns CSA2_ERR_DEVICE_CHECK when any

@@ -17,7 +17,7 @@ import torch
 from . import _build
 
 MAIN_DIM, Q_HEADS, IDX_HEADS, IDX_DIM, BLOCK, WINDOW = 512, 16, 4, 128, 8, 128
-DEV_FLAGS = {1: "INDEX_RANGE", 2: "ROW_LAYOUT", 4: "FP16_RANGE", 8: "LENGTH"}
+DEV_FLAGS = {1: "INDEX_RANGE", 2: "ROW_LAYOUT", 4: "FP16_RANGE", 8: "LENGTH", 16: "TIMEOUT", 32: "NO_TOKEN"}
 
 _lib = None
 
@@ -88,6 +88,15 @@ def lib():
             "csa2_sparse_attn_prefill_workspace_bytes": (Z, [I, I]),
             "csa2_sparse_attn_prefill": (I, [P, P, I, Cache, I64, I64, I, P, I, P, I64, F, F, P, P, P, Z, P]),
             "csa2_sparse_attn_decode_noalloc": (I, [P, Cache, P, P, P, I, P, P, P, F, P, P, P, I, P]),
+            "csa2_verify_drafts_workspace_bytes": (Z, [I, I]),
+            "csa2_verify_drafts": (I, [P, I, I64, P, I, I64, P, P, P, P, I, I, I, P, P, P, P, P, I, P, Z, P]),
+            "csa2_attn_weights_workspace_bytes": (Z, [I, I, I]),
+            "csa2_attn_weights": (I, [P, Cache, P, P, P, P, P, I, P, F, P, P, I, I, P, Z, P]),
+            "csa2_attn_weights_paged": (I, [P, Cache, P, I, I, P, P, P, P, I, P, F, P, P, I, I, P, Z, P]),
+            "csa2_cache_evict_workspace_bytes": (Z, [I, I]),
+            "csa2_cache_evict": (I, [Cache, Cache, P, P, P, P, Cache, Cache, P, P, P, P, I, I, I, I, I, P, Z, P]),
+            "csa2_cache_evict_paged": (I, [Cache, Cache, P, P, I, P, P, Cache, Cache, P, P, I, I, P, P, I, I, I, I, I,
+                                           P, Z, P]),
             "csa2_device_status": (I, [P, P, C.POINTER(C.c_uint32)]),
             "csa2_status_string": (C.c_char_p, [I]),
             "csa2_last_error": (C.c_char_p, []),
@@ -120,6 +129,7 @@ _KINDS = {
     "i32": (torch.int32, torch.uint32),                     # int32 ids / lengths, uint32 keys and flags
     "f32": (torch.float32,),
     "i64": (torch.int64, torch.uint64),
+    "prob": (torch.float32, torch.bfloat16, torch.float16),  # probabilities, with a type code beside the pointer
 }
 
 
@@ -472,3 +482,142 @@ def csa2_sparse_attn_decode_noalloc(q, main_kv, seq_row_off, seq_len, topk, win,
                                                float(sm_scale), op, lp, _arg(fn, "flags_out", flags_out, "i32", 1), B,
                                                _stream(stream))
     _check(rc, fn)
+
+
+# ----------------------------------------------------------------------------
+# after a step: verification of drafts, attention weights, eviction
+# ----------------------------------------------------------------------------
+
+_PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _launch(fn, tensors, stream, *args):
+    """Calls `fn` on the device of its tensors (which must be one device, not
+    necessarily the current one); stream None is that device's current stream."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise Csa2Error(-1, fn, f"tensors on {dev} and {t.device}")
+    f = getattr(lib(), fn)
+    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = f(*args, _stream(stream))
+    else:
+        rc = f(*args, _stream(stream))
+    _check(rc, fn)
+
+
+def _cache_tensors(*caches):
+    out = []
+    for c in caches:
+        out.extend(getattr(c, "_keep", ()) if c is not None else ())
+    return out
+
+
+def _prob_rows(fn, name, t, Q, V):
+    """(pointer, type code, row stride) of Q rows of V probabilities: fp32, bf16 or fp16, each row
+    contiguous, rows any distance apart."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _PROB_TYPES:
+        raise Csa2Error(-1, fn, f"{name}: a 2-d fp32, bf16 or fp16 tensor expected")
+    if t.shape[0] < Q or t.shape[1] != V:
+        raise Csa2Error(-1, fn, f"{name}: [{Q}, {V}] expected, got {list(t.shape)}")
+    if V > 1 and t.stride(1) != 1:
+        raise Csa2Error(-1, fn, f"{name}: the probabilities of a row must be contiguous")
+    return _arg(fn, name, t[:1, :1], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
+
+
+def csa2_verify_drafts_workspace_bytes(B, V):
+    return lib().csa2_verify_drafts_workspace_bytes(B, V)
+
+
+def csa2_verify_drafts(target, tokens, q_off, u, r, n_accept, next_tok, ws, draft=None, out_tokens=None,
+                       seq_len_in=None, seq_len_out=None, stream=None):
+    """target / draft: [Q, V] probabilities (fp32, bf16 or fp16; rows may be strided); tokens [Q]; q_off [B+1];
+    u [Q], r [B] random numbers; n_accept, next_tok [B]; out_tokens [B, M] or None."""
+    fn = "csa2_verify_drafts"
+    B, Q = n_accept.shape[0], tokens.shape[0]
+    if not isinstance(target, torch.Tensor) or target.dim() != 2:
+        raise Csa2Error(-1, fn, "target: a 2-d fp32, bf16 or fp16 tensor expected")
+    V = target.shape[1]
+    tp, tt, ts = _prob_rows(fn, "target", target, Q, V)
+    dp, dt, ds = _prob_rows(fn, "draft", draft, Q, V) if draft is not None else (None, 0, 0)
+    M = 0
+    if out_tokens is not None:
+        if out_tokens.dim() != 2 or out_tokens.shape[0] < B:
+            raise Csa2Error(-1, fn, f"out_tokens: [{B}, M] expected, got {list(out_tokens.shape)}")
+        M = out_tokens.shape[1]
+    wp, wn = _ws(ws)
+    _launch(fn, (target, draft, tokens, q_off, u, r, seq_len_in, seq_len_out, n_accept, next_tok, out_tokens, ws),
+            stream, tp, tt, ts, dp, dt, ds, _arg(fn, "tokens", tokens, "i32", Q), _arg(fn, "q_off", q_off, "i32", B + 1),
+            _arg(fn, "u", u, "f32", Q), _arg(fn, "r", r, "f32", B), B, Q, V,
+            _arg(fn, "seq_len_in", seq_len_in, "i32", B), _arg(fn, "seq_len_out", seq_len_out, "i32", B),
+            _arg(fn, "n_accept", n_accept, "i32", B), _arg(fn, "next_tok", next_tok, "i32", B),
+            _arg(fn, "out_tokens", out_tokens, "i32", B * M), M, wp, wn)
+
+
+def csa2_attn_weights_workspace_bytes(B, Q, k):
+    return lib().csa2_attn_weights_workspace_bytes(B, Q, k)
+
+
+def csa2_attn_weights(q, main_kv, seq_row_off, seq_len, topk, lse, sm_scale, acc, ws, q_off=None, n_accept=None,
+                      weights=None, stream=None):
+    """acc [main_kv.rows] fp32 += the attention weight of the selected entries; weights [Q, k] or None receives
+    the weights.  seq_row_off: [B] offsets or a PageTable; q_off / n_accept as in a verification step."""
+    paged = isinstance(seq_row_off, PageTable)
+    fn = "csa2_attn_weights_paged" if paged else "csa2_attn_weights"
+    Q, k = topk.shape
+    B = seq_len.shape[0]
+    wp, wn = _ws(ws)
+    qp = _arg(fn, "q", q, "bf16", Q * Q_HEADS * MAIN_DIM)
+    rest = (_arg(fn, "seq_len", seq_len, "i32", B), _arg(fn, "q_off", q_off, "i32", B + 1),
+            _arg(fn, "n_accept", n_accept, "i32", B), _arg(fn, "topk", topk, "i32", Q * k), k,
+            _arg(fn, "lse", lse, "f32", Q * Q_HEADS), float(sm_scale), _arg(fn, "acc", acc, "f32", main_kv.rows),
+            _arg(fn, "weights", weights, "f32", Q * k), B, Q, wp, wn)
+    where = seq_row_off.pages if paged else seq_row_off
+    tensors = (q, seq_len, q_off, n_accept, topk, lse, acc, weights, ws, where, *_cache_tensors(main_kv))
+    if paged:
+        pt = seq_row_off
+        _launch(fn, tensors, stream, qp, main_kv, _pages(fn, pt, B), pt.page_rows, pt.max_pages, *rest)
+    else:
+        _launch(fn, tensors, stream, qp, main_kv, _row_off(fn, seq_row_off, B), *rest)
+
+
+def csa2_cache_evict_workspace_bytes(B, max_len):
+    return lib().csa2_cache_evict_workspace_bytes(B, max_len)
+
+
+def csa2_cache_evict(main_src, idx_src, acc_src, src, seq_len, keep, max_len, max_keep, main_dst, idx_dst, acc_dst,
+                     dst, kept, seq_len_out, ws, first=0, last=0, stream=None):
+    """Keeps keep[b] entries of every sequence (the first `first`, the last `last`, the best others by acc_src) and
+    copies their rows to the destination.  src / dst: [B] row offsets, or a PageTable each; idx_src / idx_dst may
+    both be None; kept [B, max_keep] receives the source positions, seq_len_out [B] their number."""
+    paged = isinstance(src, PageTable)
+    fn = "csa2_cache_evict_paged" if paged else "csa2_cache_evict"
+    if paged != isinstance(dst, PageTable) or (paged and src.page_rows != dst.page_rows):
+        raise Csa2Error(-1, fn, "source and destination must both be row offsets, or page tables of one page size")
+    if (idx_src is None) != (idx_dst is None):
+        raise Csa2Error(-1, fn, "idx_src and idx_dst go together")
+    none = MXFP4Cache(None, None, 0)
+    i_src, i_dst = (none, none) if idx_src is None else (idx_src, idx_dst)
+    B = seq_len.shape[0]
+    wp, wn = _ws(ws)
+    # an accumulator per row that the caches hold
+    n_src = main_src.rows if idx_src is None else min(main_src.rows, idx_src.rows)
+    n_dst = main_dst.rows if idx_dst is None else min(main_dst.rows, idx_dst.rows)
+    ac, sl, kp = (_arg(fn, "acc_src", acc_src, "f32", n_src), _arg(fn, "seq_len", seq_len, "i32", B),
+                  _arg(fn, "keep", keep, "i32", B))
+    ad, ko, so = (_arg(fn, "acc_dst", acc_dst, "f32", n_dst), _arg(fn, "kept", kept, "i32", B * max_keep),
+                  _arg(fn, "seq_len_out", seq_len_out, "i32", B))
+    tensors = (acc_src, seq_len, keep, acc_dst, kept, seq_len_out, ws, src.pages if paged else src,
+               dst.pages if paged else dst, *_cache_tensors(main_src, idx_src, main_dst, idx_dst))
+    tail = (ko, so, B, int(max_len), int(max_keep), int(first), int(last), wp, wn)
+    if paged:
+        _launch(fn, tensors, stream, main_src, i_src, ac, _pages(fn, src, B), src.max_pages, sl, kp, main_dst, i_dst,
+                ad, _pages(fn, dst, B), dst.max_pages, src.page_rows, *tail)
+    else:
+        _launch(fn, tensors, stream, main_src, i_src, ac, _row_off(fn, src, B), sl, kp, main_dst, i_dst, ad,
+                _row_off(fn, dst, B), *tail)

@@ -811,4 +811,210 @@ csa2_status csa2_sparse_attn_prefill(const uint16_t* q, const int32_t* q_pos, in
   return check_launch(fn);
 }
 
+// ---------------------------------------------------------------------------
+namespace {
+struct VerifyWs {
+  uint32_t* status;
+  int32_t* counters;  // [B], zero between calls
+  double* part;       // [B][segments]
+  size_t bytes;
+};
+VerifyWs verify_ws(void* ws, int B, int V) {
+  Carve c(ws);
+  VerifyWs w;
+  w.status = c.take<uint32_t>(kStatusBytes / 4);
+  w.counters = c.take<int32_t>(size_t(B));
+  w.part = c.take<double>(size_t(B) * ((size_t(V) + kVerifySegment - 1) / kVerifySegment));
+  w.bytes = c.used;
+  return w;
+}
+bool prob_type_ok(int type, const void* p) {
+  if (type != CSA2_TYPE_F32 && type != CSA2_TYPE_BF16 && type != CSA2_TYPE_F16) return false;
+  return (reinterpret_cast<uintptr_t>(p) & (type == CSA2_TYPE_F32 ? 3 : 1)) == 0;
+}
+}  // namespace
+
+size_t csa2_verify_drafts_workspace_bytes(int B, int V) {
+  if (B < 0 || V < 0) return 0;
+  return verify_ws(nullptr, B, V).bytes;
+}
+
+csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t target_stride, const void* draft,
+                               int draft_type, int64_t draft_stride, const int32_t* tokens, const int32_t* q_off,
+                               const float* u, const float* r, int B, int Q, int V, const int32_t* seq_len_in,
+                               int32_t* seq_len_out, int32_t* n_accept, int32_t* next_tok, int32_t* out_tokens,
+                               int out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_verify_drafts";
+  if (B < 0 || Q < 0 || V < 1 || V > (1 << 30)) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad B, Q or V");
+  if (B == 0) return CSA2_OK;
+  if ((!target && Q > 0) || (!tokens && Q > 0) || (!u && Q > 0) || !q_off || !r || !n_accept || !next_tok ||
+      !workspace)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  if (!prob_type_ok(target_type, target) || target_stride < 0 ||
+      (draft && (!prob_type_ok(draft_type, draft) || draft_stride < 0)))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad element type, alignment or stride of target or draft");
+  if ((seq_len_in == nullptr) != (seq_len_out == nullptr))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": seq_len_in and seq_len_out go together");
+  if (out_tokens && out_stride < 1) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad out_stride");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": workspace must be 256-byte aligned");
+  const VerifyWs ws = verify_ws(workspace, B, V);
+  if (workspace_bytes < ws.bytes) return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  launch_verify(VerifyArgs{target, target_type, target_stride, draft, draft_type, draft_stride, tokens, q_off, u, r, B,
+                           Q, V, seq_len_in, seq_len_out, n_accept, next_tok, out_tokens, out_stride, ws.part,
+                           ws.counters, ws.status},
+                static_cast<cudaStream_t>(stream));
+  return check_launch(fn);
+}
+
+// ---------------------------------------------------------------------------
+size_t csa2_attn_weights_workspace_bytes(int B, int Q, int k) {
+  (void)B;
+  if (Q < 0 || k < 0) return 0;
+  Carve c(nullptr);
+  c.take<uint32_t>(kStatusBytes / 4);
+  c.take<float>(size_t(Q) * k);
+  return c.used;
+}
+
+namespace {
+csa2_status weights_args(const char* fn, const csa2_mxfp4_cache& main_kv, int B, int Q, int k) {
+  if (B < 0 || Q < 0 || k < 1 || k > CSA2_MAX_TOPK)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad B, Q or k");
+  if (Q > 0 && (B == 0 || !cache_ok(main_kv)))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad main cache, or queries without sequences");
+  return CSA2_OK;
+}
+
+csa2_status weights_impl(const char* fn, const uint16_t* q, const csa2_mxfp4_cache& main_kv, const SegDesc& sd,
+                         const int32_t* q_off, const int32_t* n_accept, const int32_t* topk, int k, const float* lse,
+                         float sm_scale, float* acc, float* weights_out, int B, int Q, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!q || !sd.len || !topk || !lse || !acc || !workspace)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  if (!q_off && (Q != B || n_accept))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": without q_off there is one query per sequence (Q == B)");
+  if (!aligned16(q) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": q must be 16-byte and workspace 256-byte aligned");
+  if (workspace_bytes < csa2_attn_weights_workspace_bytes(B, Q, k))
+    return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  Carve c(workspace);
+  uint32_t* status = c.take<uint32_t>(kStatusBytes / 4);
+  float* own = c.take<float>(size_t(Q) * k);
+  launch_weights(WeightArgs{q, main_kv.codes, main_kv.scales, sd, q_off, n_accept, topk, k, lse, sm_scale, acc,
+                            weights_out ? weights_out : own, status, B, Q},
+                 static_cast<cudaStream_t>(stream));
+  return check_launch(fn);
+}
+}  // namespace
+
+csa2_status csa2_attn_weights(const uint16_t* q, csa2_mxfp4_cache main_kv, const int64_t* seq_row_off,
+                              const int32_t* seq_len, const int32_t* q_off, const int32_t* n_accept,
+                              const int32_t* topk, int k, const float* lse, float sm_scale, float* acc,
+                              float* weights_out, int B, int Q, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  const char* fn = "csa2_attn_weights";
+  const csa2_status rc = weights_args(fn, main_kv, B, Q, k);
+  if (rc != CSA2_OK || Q == 0) return rc;
+  if (!seq_row_off) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  return weights_impl(fn, q, main_kv, SegDesc{seq_row_off, 0, seq_len, INT32_MAX, main_kv.rows}, q_off, n_accept, topk,
+                      k, lse, sm_scale, acc, weights_out, B, Q, workspace, workspace_bytes, stream);
+}
+
+csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv, const int32_t* pages, int page_rows,
+                                    int max_pages, const int32_t* seq_len, const int32_t* q_off,
+                                    const int32_t* n_accept, const int32_t* topk, int k, const float* lse,
+                                    float sm_scale, float* acc, float* weights_out, int B, int Q, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_attn_weights_paged";
+  const csa2_status rc = weights_args(fn, main_kv, B, Q, k);
+  if (rc != CSA2_OK || Q == 0) return rc;
+  int shift = 0;
+  if (!pages_ok(pages, page_rows, max_pages, main_kv.rows, main_kv.rows, &shift))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
+  return weights_impl(fn, q, main_kv, paged_desc(pages, shift, max_pages, seq_len, INT32_MAX, main_kv.rows), q_off,
+                      n_accept, topk, k, lse, sm_scale, acc, weights_out, B, Q, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+size_t csa2_cache_evict_workspace_bytes(int B, int max_len) {
+  (void)B, (void)max_len;
+  return kStatusBytes;
+}
+
+namespace {
+csa2_status evict_args(const char* fn, const EvictArgs& a, const void* acc_src, int64_t max_len, void* workspace,
+                       size_t workspace_bytes) {
+  const bool idx = a.idx_src.codes || a.idx_src.scales || a.idx_dst.codes || a.idx_dst.scales;
+  if (!cache_ok(a.main_src) || !cache_ok(a.main_dst) || (idx && (!cache_ok(a.idx_src) || !cache_ok(a.idx_dst))))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad cache");
+  if (!acc_src || !a.acc_dst || !a.src.len || !a.keep || !a.kept || !a.seq_len_out || !workspace)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  if (max_len < 0 || a.max_keep < 1 || a.first < 0 || a.last < 0)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad max_len, max_keep, first or last");
+  if (a.B > 65535) return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 sequences");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": workspace must be 256-byte aligned");
+  if (workspace_bytes < kStatusBytes) return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  return CSA2_OK;
+}
+int64_t cache_rows(const csa2_mxfp4_cache& main_kv, const csa2_mxfp4_cache& idx) {
+  return idx.codes ? (main_kv.rows < idx.rows ? main_kv.rows : idx.rows) : main_kv.rows;
+}
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+bool caches_overlap(const csa2_mxfp4_cache& s, const csa2_mxfp4_cache& d, size_t codes, size_t scales) {
+  return overlap(s.codes, size_t(s.rows) * codes, d.codes, size_t(d.rows) * codes) ||
+         overlap(s.scales, size_t(s.rows) * scales, d.scales, size_t(d.rows) * scales);
+}
+}  // namespace
+
+csa2_status csa2_cache_evict(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
+                             const int64_t* src_row_off, const int32_t* seq_len, const int32_t* keep,
+                             csa2_mxfp4_cache main_dst, csa2_mxfp4_cache idx_dst, float* acc_dst,
+                             const int64_t* dst_row_off, int32_t* kept_out, int32_t* seq_len_out, int B, int max_len,
+                             int max_keep, int first, int last, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const char* fn = "csa2_cache_evict";
+  if (B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (B == 0) return CSA2_OK;
+  if (!src_row_off || !dst_row_off) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  const int64_t srows = cache_rows(main_src, idx_src), drows = cache_rows(main_dst, idx_dst);
+  const EvictArgs a{main_src, idx_src, main_dst, idx_dst, acc_src, acc_dst,
+                    SegDesc{src_row_off, 0, seq_len, max_len, srows}, keep, dst_row_off, nullptr, 0, 0, drows,
+                    kept_out, seq_len_out, max_keep, first, last, B, static_cast<uint32_t*>(workspace)};
+  const csa2_status rc = evict_args(fn, a, acc_src, max_len, workspace, workspace_bytes);
+  if (rc != CSA2_OK) return rc;
+  if (caches_overlap(main_src, main_dst, kMainCodeBytes, kMainScaleBytes) ||
+      (idx_src.codes && caches_overlap(idx_src, idx_dst, kIdxCodeBytes, kIdxScaleBytes)) ||
+      overlap(acc_src, size_t(srows) * 4, acc_dst, size_t(drows) * 4))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": source and destination overlap");
+  return launch_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+csa2_status csa2_cache_evict_paged(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
+                                   const int32_t* pages, int max_pages, const int32_t* seq_len, const int32_t* keep,
+                                   csa2_mxfp4_cache main_dst, csa2_mxfp4_cache idx_dst, float* acc_dst,
+                                   const int32_t* dst_pages, int dst_max_pages, int page_rows, int32_t* kept_out,
+                                   int32_t* seq_len_out, int B, int max_len, int max_keep, int first, int last,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_cache_evict_paged";
+  if (B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (B == 0) return CSA2_OK;
+  const int64_t srows = cache_rows(main_src, idx_src), drows = cache_rows(main_dst, idx_dst);
+  int shift = 0;
+  if (!pages_ok(pages, page_rows, max_pages, main_src.rows, srows, &shift) ||
+      !pages_ok(dst_pages, page_rows, dst_max_pages, main_dst.rows, drows, &shift))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
+  const EvictArgs a{main_src, idx_src, main_dst, idx_dst, acc_src, acc_dst,
+                    paged_desc(pages, shift, max_pages, seq_len, max_len, srows), keep, nullptr, dst_pages, shift,
+                    dst_max_pages, drows, kept_out, seq_len_out, max_keep, first, last, B,
+                    static_cast<uint32_t*>(workspace)};
+  const csa2_status rc = evict_args(fn, a, acc_src, max_len, workspace, workspace_bytes);
+  if (rc != CSA2_OK) return rc;
+  return launch_evict(a, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -255,4 +255,70 @@ struct CompressArgs {
 };
 void launch_compress(const CompressArgs& a, cudaStream_t st);
 
+// Verification of drafted tokens: per sequence the accepted prefix of its
+// candidates and the next token.
+constexpr int kVerifySegment = 1024;  // vocabulary entries of one partial sum
+struct VerifyArgs {
+  const void* target;      // [Q] rows of V, CSA2_TYPE_* elements
+  int target_type;
+  int64_t target_stride;   // elements
+  const void* draft;       // [Q] rows of V, or null
+  int draft_type;
+  int64_t draft_stride;
+  const int32_t* tokens;   // [Q]
+  const int32_t* q_off;    // [B+1]
+  const float* u;          // [Q]
+  const float* r;          // [B]
+  int B, Q, V;
+  const int32_t* seq_len_in;   // [B] or null
+  int32_t* seq_len_out;        // [B] or null (may be seq_len_in)
+  int32_t* n_accept;       // [B]
+  int32_t* next_tok;       // [B]
+  int32_t* out_tokens;     // [B][out_stride] or null
+  int out_stride;
+  double* part;            // workspace: [B][ceil(V / kVerifySegment)] sums
+  int32_t* counters;       // [B] arrival counters, zero between calls
+  uint32_t* status;
+};
+void launch_verify(const VerifyArgs& a, cudaStream_t st);
+
+// Attention weight of selected entries, added to the entries' accumulators.
+struct WeightArgs {
+  const uint16_t* q;        // [Q][16][512] bf16
+  const uint8_t* mcodes;
+  const uint8_t* mscales;
+  SegDesc sd;               // rows of sequence b
+  const int32_t* q_off;     // [B+1], or null: query i is sequence i's
+  const int32_t* n_accept;  // [B] or null: queries 0 .. n_accept[b] of a sequence count
+  const int32_t* topk;      // [Q][k]
+  int k;
+  const float* lse;         // [Q][16]
+  float sm_scale;
+  float* acc;               // [cache rows]
+  float* weights;           // [Q][k]
+  uint32_t* status;
+  int B, Q;
+};
+void launch_weights(const WeightArgs& a, cudaStream_t st);
+
+// Eviction by accumulated weight: the kept positions of every sequence, then
+// their rows moved to the destination.
+struct EvictArgs {
+  csa2_mxfp4_cache main_src, idx_src, main_dst, idx_dst;  // idx codes null: no indexer cache
+  const float* acc_src;
+  float* acc_dst;
+  SegDesc src;                 // rows of sequence b, and its length
+  const int32_t* keep;         // [B]
+  const int64_t* dst_row_off;  // [B], or the page table below
+  const int32_t* dst_pages;    // [B][dst_max_pages]
+  int dst_shift;
+  int dst_max_pages;
+  int64_t dst_rows;
+  int32_t* kept;               // [B][max_keep]
+  int32_t* seq_len_out;        // [B] (may be the source lengths themselves)
+  int max_keep, first, last, B;
+  uint32_t* status;
+};
+csa2_status launch_evict(const EvictArgs& a, cudaStream_t st);
+
 }  // namespace csa2

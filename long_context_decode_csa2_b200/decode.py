@@ -29,9 +29,16 @@ carries up to Q queries in total, a ragged number per sequence (``q_off``),
 each with its own visible entry count (``q_vis``).  The scanning Full layer
 reads every sequence's indexer K once for all of its queries
 (``csa2_index_multi``); the later calls take the queries as Q segments.
+
+After a step: ``DecodeStep.verify`` decides which candidates of a verification
+step stand and draws the next tokens, ``DecodeStep.accumulate`` adds the
+attention weight that every layer gave its selection to the caches'
+accumulators (``FullCache.acc``), and ``evict`` cuts caches down to the
+entries that carried the most of it.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from dataclasses import dataclass
 
@@ -42,8 +49,25 @@ from . import csa2 as C
 
 @dataclass
 class FullCache:
+    """One Full layer's caches; acc ([rows] fp32, optional) accumulates the
+    attention weight of the entries (zero for entries not yet attended)."""
+
     idx: C.MXFP4Cache
     main: C.MXFP4Cache
+    acc: torch.Tensor | None = None
+
+
+def evict(src: FullCache, dst: FullCache, src_rows, dst_rows, seq_len, keep, max_len: int, max_keep: int, kept,
+          seq_len_out, ws, first: int = 0, last: int = C.WINDOW, stream=None):
+    """Cuts every sequence of ``src`` to keep[b] entries (the first ``first``,
+    the last ``last`` and the most attended others) and copies them, in order,
+    to ``dst``.  src_rows / dst_rows: row offsets, or page tables of one pool.
+    kept [B, max_keep] receives the kept positions, seq_len_out [B] their
+    number.  ``ws``: csa2_cache_evict_workspace_bytes(B, max_len) bytes."""
+    if src.acc is None or dst.acc is None:
+        raise ValueError("eviction ranks entries by FullCache.acc: both caches need one")
+    C.csa2_cache_evict(src.main, src.idx, src.acc, src_rows, seq_len, keep, max_len, max_keep, dst.main, dst.idx,
+                       dst.acc, dst_rows, kept, seq_len_out, ws, first=first, last=last, stream=stream)
 
 
 def layer_plan(pattern: str, full_rescan: bool = False):
@@ -175,6 +199,9 @@ class DecodeStep:
         # ratio 2: one pending-token state per Full layer's caches
         n_full = sum(1 for m in pattern if m == "F")
         self.pairs = [PairStream(B, dev, projection) for _ in range(n_full)] if ratio == 2 else []
+        # after-step calls (verify, accumulate): made at their first use
+        self.ws_verify = self.ws_weights = None
+        self.n_accept = self.next_tok = None
         # optional callable(call_name, "begin" | "end", stream), e.g. to record events
         self.hook = None
 
@@ -370,6 +397,51 @@ class DecodeStep:
             main.wait_event(self.ev_group[self.plan[-1][0]][g])
         return self.out
 
+    @staticmethod
+    def _filling(stream):
+        """Scratch made at its first use is zero-filled on the stream that uses it."""
+        return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+
+    def verify(self, target, tokens, q_off, u, r, draft=None, seq_len=None, out_tokens=None, stream=None):
+        """After a verification step: which candidates stand, and the next
+        token of every sequence (``csa2_verify_drafts``).  target / draft
+        [Q, V] probabilities behind / for every candidate, tokens [Q], u [Q]
+        and r [B] random numbers.  seq_len [B], if given, holds the lengths
+        with all candidates appended and drops the rejected ones in place.
+        Returns (n_accept, next_tok), tensors that the next call overwrites."""
+        if self.queries is None:
+            raise ValueError("verify goes with a verification step (queries=Q)")
+        need = C.csa2_verify_drafts_workspace_bytes(self.B, target.shape[1])
+        with self._filling(stream):
+            if self.ws_verify is None or self.ws_verify.numel() < need:
+                self.ws_verify = C.workspace(need, self.out.device)
+            if self.n_accept is None:
+                self.n_accept = torch.zeros(self.B, dtype=torch.int32, device=self.out.device)
+                self.next_tok = torch.zeros(self.B, dtype=torch.int32, device=self.out.device)
+        C.csa2_verify_drafts(target, tokens, q_off, u, r, self.n_accept, self.next_tok, self.ws_verify, draft=draft,
+                             out_tokens=out_tokens, seq_len_in=seq_len, seq_len_out=seq_len, stream=stream)
+        return self.n_accept, self.next_tok
+
+    def accumulate(self, caches, seq_row_off, seq_len, layers, q_off=None, n_accept=None, stream=None):
+        """After ``run``: adds the attention weight of every layer's selection
+        to its Full layer's ``FullCache.acc`` (``csa2_attn_weights``), layer by
+        layer.  Verification steps pass q_off, and n_accept (from ``verify``)
+        to count only the candidates that stand; seq_len may then be the
+        lengths without the rejected ones."""
+        if (self.queries is None) != (q_off is None):
+            raise ValueError("q_off goes with (and only with) a verification step")
+        nq = self.topk[0].shape[0]
+        if self.ws_weights is None:
+            with self._filling(stream):
+                self.ws_weights = C.workspace(C.csa2_attn_weights_workspace_bytes(self.B, nq, self.k),
+                                              self.out.device)
+        for layer, _, f, _ in self.plan:
+            if caches[f].acc is None:
+                raise ValueError("accumulate needs FullCache.acc")
+            C.csa2_attn_weights(layers[layer]["q"], caches[f].main, seq_row_off, seq_len, self.topk[layer],
+                                self.lse[layer], self.sm_scale, caches[f].acc, self.ws_weights, q_off=q_off,
+                                n_accept=n_accept, stream=stream)
+
     def capture(self, caches, seq_row_off, seq_len, layers, new_tokens=None, q_off=None, q_vis=None):
         """Records one step into a CUDA graph; ``graph.replay()`` then runs the
         whole step (every call, both schedules, with the same buffers) as one
@@ -389,7 +461,7 @@ class DecodeStep:
 
     def device_flags(self) -> int:
         flags = C.device_status(self.ws_full)
-        extra = [p.ws for p in self.pairs]
+        extra = [p.ws for p in self.pairs] + [self.ws_verify, self.ws_weights]
         flat = []
         for w in self.ws_re + self.ws_attn:
             flat.extend(w if isinstance(w, list) else [w])
