@@ -952,7 +952,8 @@ csa2_status evict_args(const char* fn, const EvictArgs& a, const void* acc_src, 
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
   if (max_len < 0 || a.max_keep < 1 || a.first < 0 || a.last < 0)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad max_len, max_keep, first or last");
-  if (a.B > 65535) return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 sequences");
+  if (a.B > 65535 || max_len > (1 << 30) || a.max_keep > (1 << 30))
+    return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 sequences or 2^30 entries");
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": workspace must be 256-byte aligned");
   if (workspace_bytes < kStatusBytes) return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
