@@ -8,15 +8,17 @@
 //
 // k_evict_select finds the kept positions, a cluster of C CTAs per sequence.
 // Each CTA owns a run of positions and each of its warps a part of the run,
-// whose rank keys it holds in shared memory as far as there is room (the rest
+// whose weights it holds in shared memory as far as there is room (the rest
 // is read again, from L2 as a rule).  Most entries of a long cache were never
 // selected and stand at exactly 0, so the first pass only counts the entries
 // above 0 and at 0: where that puts the threshold at 0 it is known, and so
 // are every warp's counts above and at it.  Otherwise the cluster counts the
-// keys of the threshold's sign by digits of 11, 10 and 10 bits and adds the
-// histograms through distributed shared memory; once the threshold's bin
-// holds at most 1024 keys, every CTA collects them and the one sought is
-// found by counting.  Then each warp writes its kept positions in order.
+// entries of the threshold's sign by digits of 11, 10 and 10 bits and adds
+// the histograms through distributed shared memory; once the threshold's bin
+// holds at most 1024 entries, every CTA collects them and goes on alone.
+// Then each warp writes its kept positions in order.  Bound by instructions
+// (an entry is 4 bytes): the passes compare floats, and the ordered write
+// scans the flags of 128 positions at once, four counts to a register.
 //
 // k_evict_move copies the rows: a CTA takes a run of destination rows, so its
 // writes are contiguous and every CTA moves the same amount whatever the
@@ -40,24 +42,23 @@ constexpr int kEWarps = kEThreads / 32;
 constexpr int kStep = 128;                    // positions of a warp's step, 4 per lane
 constexpr int kBatch = 4;                     // steps whose loads are in flight together
 constexpr int kBins = 2048;
-constexpr int kList = kEThreads;              // keys of the threshold's bin that are ranked one per thread
+constexpr int kList = kEThreads;              // entries of the threshold's bin that every CTA finishes alone
 constexpr int kMaxCluster = 16;
 constexpr int kRunKeys = 8192;                // positions per CTA that are worth a CTA
-constexpr uint32_t kZeroKey = 0x80000000u;    // rank key of an entry that was never selected
 
 struct __align__(16) SelSmem {
   uint32_t hist[kBins];       // this CTA's counts of the current digit
   uint32_t total[kBins];      // the cluster's
-  uint32_t list[kList];       // this CTA's keys in the threshold's bin
+  uint32_t list[kList];       // this CTA's entries of the threshold's bin
   uint32_t all[kList];        // the cluster's
   uint32_t scan[kEWarps];
   uint32_t listed, gathered;
-  uint32_t bin, above, thr, take;
-  uint32_t warp_gt[kEWarps], warp_eq[kEWarps];  // every warp's keys above the threshold (first: 0) and at it
+  uint32_t bin, above;
+  uint32_t warp_gt[kEWarps], warp_eq[kEWarps];  // every warp's entries above the threshold (first: 0) and at it
   uint32_t gt[2][kMaxCluster], eq[2][kMaxCluster];  // every CTA's: above and at 0, above and at the threshold
 };
 
-static_assert(sizeof(SelSmem) % 16 == 0, "the keys behind it are read as 16-byte words");
+static_assert(sizeof(SelSmem) % 16 == 0, "the weights behind it are read as 16-byte words");
 
 // What stays of sequence b.
 struct Plan {
@@ -98,25 +99,9 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v, int lane) {
   return v;
 }
 
-// Rank keys of positions p .. p+3 (p a multiple of 4) of sequence b; 0 where a
-// position does not compete (outside [m0, m1)).  Four positions never cross a
-// page or the end of the accumulators, whose rows come in groups of 8.
-__device__ __forceinline__ float4 load_acc(const EvictArgs& a, int b, int p, int m0, int m1, bool vec) {
-  if (p + 4 <= m0 || p >= m1) return make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* src = a.acc_src + seg_row(a.src, b, p, a.status);
-  if (vec) return __ldg(reinterpret_cast<const float4*>(src));
-  return make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
-}
-__device__ __forceinline__ uint4 keys4(float4 f, int p, int m0, int m1) {
-  uint4 k = make_uint4(rank_key(f.x), rank_key(f.y), rank_key(f.z), rank_key(f.w));
-  if (p < m0 || p + 4 > m1) {
-    if (p < m0 || p >= m1) k.x = 0;
-    if (p + 1 < m0 || p + 1 >= m1) k.y = 0;
-    if (p + 2 < m0 || p + 2 >= m1) k.z = 0;
-    if (p + 3 < m0 || p + 3 >= m1) k.w = 0;
-  }
-  return k;
-}
+// 31-bit rank of a weight among those of its sign: of a positive one its bits,
+// of a negative one or a NaN its rank key (NaN lowest).
+__device__ __forceinline__ uint32_t side_key(float f, bool neg) { return neg ? rank_key(f) : __float_as_uint(f); }
 
 __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int warp_cap) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -124,7 +109,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   cg::cluster_group cl = cg::this_cluster();
   const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* mine = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SelSmem)) + warp * warp_cap;  // this warp's keys
+  float* mine = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem)) + warp * warp_cap;  // this warp's weights
   const bool vec = (reinterpret_cast<uintptr_t>(a.acc_src) & 15) == 0;
   launch_dependents();
   for (int i = tid; i < kBins; i += kEThreads) sm.hist[i] = 0;
@@ -147,61 +132,56 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   const int s0 = int(int64_t(steps) * rank / C), s1 = int(int64_t(steps) * (rank + 1) / C);
   const int w0 = (s0 + int(int64_t(s1 - s0) * warp / kEWarps)) * kStep;
   const int w1 = min(len, (s0 + int(int64_t(s1 - s0) * (warp + 1) / kEWarps)) * kStep);
-  // ---- the keys, and how many lie above 0 and at 0 ----
-  {
-    uint32_t pos = 0, zer = 0;
-    for (int q0 = w0; q0 < w1; q0 += kBatch * kStep) {
+  const int wc = min(w1, w0 + warp_cap);
+  const float* base = a.src.pages ? nullptr : a.acc_src + a.src.row_off[b];
+  // (a step never crosses a page)
+  auto step_at = [&](int q0) { return base ? base + q0 : a.acc_src + seg_row(a.src, b, q0, a.status); };
+  // The whole warp over its part from `from`, 4 consecutive positions per
+  // lane: fn(position, four weights), kBatch steps' loads in flight.
+  // Accumulators come in groups of 8, so the four lie inside them; positions
+  // behind the end of the sequence and protected ones are for fn to leave out.
+  auto from_global = [&](int from, auto&& fn) {
+    for (int q0 = from; q0 < w1; q0 += kBatch * kStep) {
       float4 f[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kStep + 4 * lane;
-        f[i] = q < w1 ? load_acc(a, b, q, m0, m1, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int q = q0 + i * kStep + 4 * lane;
         if (q < w1) {
-          const uint4 k = keys4(f[i], q, m0, m1);
-          if (q - w0 < warp_cap) *reinterpret_cast<uint4*>(mine + (q - w0)) = k;
-          pos += uint32_t(k.x > kZeroKey) + uint32_t(k.y > kZeroKey) + uint32_t(k.z > kZeroKey) +
-                 uint32_t(k.w > kZeroKey);
-          zer += uint32_t(k.x == kZeroKey) + uint32_t(k.y == kZeroKey) + uint32_t(k.z == kZeroKey) +
-                 uint32_t(k.w == kZeroKey);
+          const float* src = step_at(q0 + i * kStep) + 4 * lane;
+          f[i] = vec ? __ldg(reinterpret_cast<const float4*>(src))
+                     : make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
         }
       }
-    }
-    pos = __reduce_add_sync(0xffffffffu, pos);
-    zer = __reduce_add_sync(0xffffffffu, zer);
-    if (lane == 0) {
-      sm.warp_gt[warp] = pos;
-      sm.warp_eq[warp] = zer;
-    }
-  }
-  // every later pass over this warp's keys, the whole warp at a time:
-  // fn(this lane's first position, its four keys); a key 0 does not compete
-  auto each = [&](auto&& fn) {
-    const int wc = min(w1, w0 + warp_cap);
-    for (int q0 = w0; q0 < wc; q0 += kStep) {
-      const int q = q0 + 4 * lane;
-      fn(q, q < wc ? *reinterpret_cast<const uint4*>(mine + (q - w0)) : make_uint4(0, 0, 0, 0));
-    }
-    for (int q0 = w0 + warp_cap; q0 < w1; q0 += kBatch * kStep) {
-      float4 f[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kStep + 4 * lane;
-        f[i] = q < w1 ? load_acc(a, b, q, m0, m1, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kStep + 4 * lane;
-        if (q0 + i * kStep < w1) fn(q, q < w1 ? keys4(f[i], q, m0, m1) : make_uint4(0, 0, 0, 0));
-      }
+      for (int i = 0; i < kBatch; ++i)
+        if (q0 + i * kStep + 4 * lane < w1) fn(q0 + i * kStep + 4 * lane, f[i]);
     }
   };
-  // Sums sm.warp_gt / warp_eq over the cluster; slot 0: above and at 0, slot
-  // 1: above and at the threshold.
-  auto share = [&](int slot) {
+  auto each = [&](auto&& fn) {
+#pragma unroll 2
+    for (int q = w0 + 4 * lane; q < wc; q += kStep) fn(q, *reinterpret_cast<const float4*>(mine + (q - w0)));
+    from_global(w0 + warp_cap, fn);
+  };
+  // fn(weight) for those of the four that compete.
+  auto competing = [&](int q, float4 f, auto&& fn) {
+    if (q >= m0 && q + 4 <= m1) {
+      fn(f.x), fn(f.y), fn(f.z), fn(f.w);
+    } else {
+      if (q >= m0 && q < m1) fn(f.x);
+      if (q + 1 >= m0 && q + 1 < m1) fn(f.y);
+      if (q + 2 >= m0 && q + 2 < m1) fn(f.z);
+      if (q + 3 >= m0 && q + 3 < m1) fn(f.w);
+    }
+  };
+  // Sums every warp's (gt, eq) over the CTA and hands the sums to the cluster;
+  // slot 0: above and at 0, slot 1: above and at the threshold.
+  auto share = [&](int slot, uint32_t gt, uint32_t eq) {
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      sm.warp_gt[warp] = gt;
+      sm.warp_eq[warp] = eq;
+    }
     __syncthreads();
     if (warp == 0) {
       const uint32_t g = __reduce_add_sync(0xffffffffu, sm.warp_gt[lane]);
@@ -213,158 +193,207 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
     }
     cl.sync();
   };
-  share(0);
+  uint32_t gt = 0, eq = 0;
+  // ---- the weights, and how many lie above 0 and at 0 ----
+  from_global(w0, [&](int q, float4 f) {
+    if (q < wc) *reinterpret_cast<float4*>(mine + (q - w0)) = f;
+    competing(q, f, [&](float x) {
+      gt += x > 0.0f;
+      eq += x == 0.0f;
+    });
+  });
+  share(0, gt, eq);
   int slot = 0;
-  uint32_t left = uint32_t(p.need), thr = kZeroKey;
-  {
-    const uint32_t P = __reduce_add_sync(0xffffffffu, lane < C ? sm.gt[0][lane] : 0u);
-    const uint32_t Z = __reduce_add_sync(0xffffffffu, lane < C ? sm.eq[0][lane] : 0u);
-    if (left > P && left <= P + Z) {
-      left -= P;  // the threshold is 0: so many of the zeros stay
-    } else {
-      // ---- the threshold's key, digit by digit among the keys of its sign ----
-      slot = 1;
-      const bool neg = left > P;
-      if (neg) left -= P + Z;
-      thr = neg ? 0u : kZeroKey;
-      uint32_t mask = 0x80000000u;  // the bits of the threshold that are known
-      auto in_bin = [&](uint32_t k) { return (k & mask) == thr && k != kZeroKey && k != 0u; };
-      for (int digit = 0; digit < 3; ++digit) {
-        const int shift = digit == 0 ? 20 : digit == 1 ? 10 : 0;
-        const uint32_t width = digit == 0 ? 2047u : 1023u;
-        each([&](int, uint4 k) {
-          if (in_bin(k.x)) atomicAdd(&sm.hist[(k.x >> shift) & width], 1u);
-          if (in_bin(k.y)) atomicAdd(&sm.hist[(k.y >> shift) & width], 1u);
-          if (in_bin(k.z)) atomicAdd(&sm.hist[(k.z >> shift) & width], 1u);
-          if (in_bin(k.w)) atomicAdd(&sm.hist[(k.w >> shift) & width], 1u);
+  uint32_t left = uint32_t(p.need);
+  float thr = 0.0f;  // the threshold (NaN: NaN entries are the least that stay)
+  const uint32_t above0 = __reduce_add_sync(0xffffffffu, lane < C ? sm.gt[0][lane] : 0u);
+  const uint32_t at0 = __reduce_add_sync(0xffffffffu, lane < C ? sm.eq[0][lane] : 0u);
+  if (left > above0 && left <= above0 + at0) {
+    left -= above0;  // the threshold is 0: so many of the zeros stay
+  } else {
+    // ---- the threshold, digit by digit among the entries of its sign ----
+    slot = 1;
+    const bool neg = left > above0;
+    if (neg) left -= above0 + at0;
+    uint32_t known = 0, mask = 0;  // the threshold's rank, and which bits of it are known
+    // The bin of `counts` that holds the left-th largest, among bins that
+    // thread t owns (2047 - 2t and 2046 - 2t); zeroes the histogram.
+    auto find = [&](const uint32_t* counts, int shift, uint32_t width) {
+      const uint32_t v0 = counts[kBins - 1 - 2 * tid], v1 = counts[kBins - 2 - 2 * tid];
+      const uint32_t incl = warp_incl(v0 + v1, lane);
+      if (lane == 31) sm.scan[warp] = incl;
+      sm.hist[kBins - 1 - 2 * tid] = sm.hist[kBins - 2 - 2 * tid] = 0;
+      __syncthreads();
+      const uint32_t part = warp_incl(sm.scan[lane], lane);
+      uint32_t prior = __shfl_sync(0xffffffffu, part, (warp + 31) & 31);
+      prior = (warp ? prior : 0u) + incl - v0 - v1;
+      if (prior < left && prior + v0 + v1 >= left) {
+        const bool second = prior + v0 < left;
+        sm.bin = uint32_t(kBins - 1 - 2 * tid - (second ? 1 : 0));
+        sm.above = prior + (second ? v0 : 0u);
+      }
+      __syncthreads();
+      left -= sm.above;
+      known |= sm.bin << shift;
+      mask |= width << shift;
+    };
+    constexpr int kShift[3] = {20, 10, 0};
+    int digit = 0;
+    bool alone = false;
+    uint32_t x = 0, n = 0;  // alone: this thread's entry of the bin, and how many there are
+    for (; digit < 3 && !alone; ++digit) {
+      const int shift = kShift[digit];
+      const uint32_t width = digit == 0 ? 2047u : 1023u;
+      each([&](int q, float4 f) {
+        competing(q, f, [&](float y) {
+          if (neg ? !(y >= 0.0f) : y > 0.0f) {
+            const uint32_t k = side_key(y, neg);
+            if ((k & mask) == known) atomicAdd(&sm.hist[(k >> shift) & width], 1u);
+          }
         });
-        // CTA r adds its share of the bins over the cluster and hands the sums to all
-        cl.sync();
-        const int per = (kBins + C - 1) / C;
-        for (int i = tid; i < per && rank * per + i < kBins; i += kEThreads) {
-          uint32_t v = 0;
-#pragma unroll 4
-          for (int c = 0; c < C; ++c) v += cl.map_shared_rank(sm.hist, c)[rank * per + i];
-#pragma unroll 4
-          for (int c = 0; c < C; ++c) cl.map_shared_rank(sm.total, c)[rank * per + i] = v;
-        }
-        cl.sync();
-        // the bin that holds the left-th largest key: thread t owns bins 2047 - 2t and 2046 - 2t
-        const uint32_t v0 = sm.total[kBins - 1 - 2 * tid], v1 = sm.total[kBins - 2 - 2 * tid];
-        const uint32_t incl = warp_incl(v0 + v1, lane);
-        if (lane == 31) sm.scan[warp] = incl;
-        for (int i = tid; i < kBins; i += kEThreads) sm.hist[i] = 0;
-        __syncthreads();
-        const uint32_t part = warp_incl(sm.scan[lane], lane);
-        uint32_t before = __shfl_sync(0xffffffffu, part, (warp + 31) & 31);
-        before = (warp ? before : 0u) + incl - v0 - v1;
-        if (before < left && before + v0 + v1 >= left) {
-          const bool second = before + v0 < left;
-          sm.bin = uint32_t(kBins - 1 - 2 * tid - (second ? 1 : 0));
-          sm.above = before + (second ? v0 : 0u);
-        }
-        __syncthreads();
-        left -= sm.above;
-        thr |= sm.bin << shift;
-        mask |= width << shift;
-        if (digit == 2) break;
-        const uint32_t inbin = sm.total[sm.bin];
-        if (inbin <= uint32_t(kList)) {
-          // few enough: every CTA gathers them and ranks one per thread
-          each([&](int, uint4 k) {
-            if (in_bin(k.x)) sm.list[atomicAdd(&sm.listed, 1u)] = k.x;
-            if (in_bin(k.y)) sm.list[atomicAdd(&sm.listed, 1u)] = k.y;
-            if (in_bin(k.z)) sm.list[atomicAdd(&sm.listed, 1u)] = k.z;
-            if (in_bin(k.w)) sm.list[atomicAdd(&sm.listed, 1u)] = k.w;
-          });
-          cl.sync();
-          const int group = kEThreads / C, src = tid / group;
-          if (src < C) {
-            const uint32_t n = *cl.map_shared_rank(&sm.listed, src);
-            const uint32_t* from = cl.map_shared_rank(sm.list, src);
-            for (uint32_t i = tid % group; i < n; i += group) sm.all[atomicAdd(&sm.gathered, 1u)] = from[i];
-          }
-          __syncthreads();
-          if (tid < int(inbin)) {
-            const uint32_t x = sm.all[tid];
-            uint32_t gt = 0, eq = 0;
-            for (uint32_t i = 0; i < inbin; ++i) {
-              const uint32_t y = sm.all[i];
-              gt += y > x;
-              eq += y == x;
-            }
-            if (gt < left && gt + eq >= left) {  // (equal keys write the same values)
-              sm.thr = x;
-              sm.take = left - gt;
-            }
-          }
-          __syncthreads();
-          thr = sm.thr;
-          left = sm.take;
-          break;
-        }
-      }
-      // ---- keys above and at the threshold ----
-      uint32_t gt = 0, eq = 0;
-      each([&](int, uint4 k) {
-        gt += uint32_t(k.x > thr) + uint32_t(k.y > thr) + uint32_t(k.z > thr) + uint32_t(k.w > thr);
-        eq += uint32_t(k.x == thr) + uint32_t(k.y == thr) + uint32_t(k.z == thr) + uint32_t(k.w == thr);
       });
-      gt = __reduce_add_sync(0xffffffffu, gt);
-      eq = __reduce_add_sync(0xffffffffu, eq);
-      if (lane == 0) {
-        sm.warp_gt[warp] = gt;
-        sm.warp_eq[warp] = eq;
+      // CTA r adds its share of the bins over the cluster and hands the sums to all
+      cl.sync();
+      const int per = (kBins + C - 1) / C;
+      for (int i = tid; i < per && rank * per + i < kBins; i += kEThreads) {
+        uint32_t v = 0;
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) v += cl.map_shared_rank(sm.hist, c)[rank * per + i];
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) cl.map_shared_rank(sm.total, c)[rank * per + i] = v;
       }
-      share(1);
+      cl.sync();
+      find(sm.total, shift, width);
+      n = sm.total[sm.bin];
+      alone = digit < 2 && n <= uint32_t(kList);
     }
+    if (alone) {
+      each([&](int q, float4 f) {
+        competing(q, f, [&](float y) {
+          if (neg ? !(y >= 0.0f) : y > 0.0f) {
+            const uint32_t k = side_key(y, neg);
+            if ((k & mask) == known) sm.list[atomicAdd(&sm.listed, 1u)] = k;
+          }
+        });
+      });
+      cl.sync();
+      const int group = kEThreads / C, src = tid / group;
+      if (src < C) {
+        const uint32_t m = *cl.map_shared_rank(&sm.listed, src);
+        const uint32_t* from = cl.map_shared_rank(sm.list, src);
+        for (uint32_t i = tid % group; i < m; i += group) sm.all[atomicAdd(&sm.gathered, 1u)] = from[i];
+      }
+      __syncthreads();
+      x = uint32_t(tid) < n ? sm.all[tid] : 0u;
+      for (; digit < 3; ++digit) {
+        const int shift = kShift[digit];
+        if (uint32_t(tid) < n && (x & mask) == known) atomicAdd(&sm.hist[(x >> shift) & 1023u], 1u);
+        __syncthreads();
+        find(sm.hist, shift, 1023u);
+      }
+    }
+    thr = neg ? (known == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(~known)) : __uint_as_float(known);
+    // ---- entries above and at the threshold ----
+    gt = eq = 0;
+    if (thr == thr) {
+      each([&](int q, float4 f) {
+        competing(q, f, [&](float y) {
+          gt += y > thr;
+          eq += y == thr;
+        });
+      });
+    } else {
+      each([&](int q, float4 f) {
+        competing(q, f, [&](float y) {
+          gt += y == y;
+          eq += y != y;
+        });
+      });
+    }
+    share(1, gt, eq);
   }
   // (that barrier followed the last access to another CTA's memory, and every
   // CTA's read of the length: seq_len_out may be seq_len itself)
   if (rank == 0 && tid == 0) a.seq_len_out[b] = p.n;
-  const uint32_t take_eq = left;  // of the keys equal to the threshold, how many stay
-  // ---- the ordered list: what precedes this warp's part, then 32 positions at a time ----
-  uint32_t ng = __reduce_add_sync(0xffffffffu, (lane < rank ? sm.gt[slot][lane] : 0u) +
-                                                   (lane < warp ? sm.warp_gt[lane] : 0u));
+  const uint32_t take_eq = left;  // of the entries at the threshold, how many stay
+  const bool nan_thr = thr != thr;
+  // ---- the ordered list: what precedes this warp's part, then 128 positions at a time ----
+  const uint32_t ng = __reduce_add_sync(0xffffffffu, (lane < rank ? sm.gt[slot][lane] : 0u) +
+                                                         (lane < warp ? sm.warp_gt[lane] : 0u));
   uint32_t ne = __reduce_add_sync(0xffffffffu, (lane < rank ? sm.eq[slot][lane] : 0u) +
                                                    (lane < warp ? sm.warp_eq[lane] : 0u));
   uint32_t at = ng + uint32_t(min(w0, m0)) + uint32_t(max(0, w0 - m1)) + min(ne, take_eq);  // kept before w0
   const uint32_t below = (1u << lane) - 1u;
-  auto emit = [&](int q0, uint32_t k) {
-    const int q = q0 + lane;
-    bool stays = k > thr;
-    if (q0 < m0 || q0 + 32 > m1) stays = stays || q < m0 || (q >= m1 && q < len);
-    if (ne < take_eq) {
-      const uint32_t same = __ballot_sync(0xffffffffu, k == thr);
-      stays = stays || (k == thr && ne + __popc(same & below) < take_eq);
-      ne += __popc(same);
+  // f[i]: the weight of position q0 + 32 i + lane (any value behind the end)
+  auto emit = [&](int q0, const float (&f)[4]) {
+    bool stays[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) stays[i] = f[i] > thr;
+    if (nan_thr || q0 < m0 || q0 + kStep > m1) {
+      // some of these 128 are protected or behind the end
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = q0 + 32 * i + lane;
+        const bool in = q >= m0 && q < m1;
+        const bool same = in && (nan_thr ? f[i] != f[i] : f[i] == thr);
+        const uint32_t m = __ballot_sync(0xffffffffu, same);
+        stays[i] = in ? (nan_thr ? f[i] == f[i] : stays[i]) || (same && ne + __popc(m & below) < take_eq) : q < len;
+        ne += __popc(m);
+      }
+    } else if (ne < take_eq) {
+      // the first entries at the threshold stay: as a rule all of these 128
+      const uint32_t n = __reduce_add_sync(0xffffffffu, uint32_t(f[0] == thr) + uint32_t(f[1] == thr) +
+                                                            uint32_t(f[2] == thr) + uint32_t(f[3] == thr));
+      if (ne + n <= take_eq) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) stays[i] = f[i] >= thr;
+        ne += n;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = __ballot_sync(0xffffffffu, f[i] == thr);
+          stays[i] = stays[i] || (f[i] == thr && ne + __popc(m & below) < take_eq);
+          ne += __popc(m);
+        }
+      }
     }
-    const uint32_t all = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept[at + __popc(all & below)] = q;
-    at += __popc(all);
+    const uint32_t flags = uint32_t(stays[0]) | uint32_t(stays[1]) << 8 | uint32_t(stays[2]) << 16 |
+                           uint32_t(stays[3]) << 24;
+    const uint32_t incl = warp_incl(flags, lane), sum = __shfl_sync(0xffffffffu, incl, 31);
+    // four indexes from `at` (each below 128): entries of earlier groups of 32, and of lanes below
+    const uint32_t idx = incl - flags + sum * 0x01010100u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (stays[i]) kept[at + ((idx >> (8 * i)) & 255u)] = q0 + 32 * i + lane;
+    at += (sum * 0x01010101u) >> 24;
   };
-  const int wc = min(w1, w0 + warp_cap);
-#pragma unroll 4
-  for (int q0 = w0; q0 < wc; q0 += 32) emit(q0, q0 + lane < wc ? mine[q0 - w0 + lane] : 0u);
-  for (int q0 = w0 + warp_cap; q0 < w1; q0 += 8 * 32) {
-    float f[8];
+  for (int q0 = w0; q0 < wc; q0 += kStep) {
+    float f[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = q0 + 32 * i + lane;
-      f[i] = q >= m0 && q < min(w1, m1) ? __ldg(a.acc_src + seg_row(a.src, b, q, a.status)) : 0.0f;
-    }
+    for (int i = 0; i < 4; ++i) f[i] = mine[q0 - w0 + 32 * i + lane];
+    emit(q0, f);
+  }
+  for (int q0 = w0 + warp_cap; q0 < w1; q0 += 2 * kStep) {
+    float f[2][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = q0 + 32 * i + lane;
-      if (q0 + 32 * i < w1) emit(q0 + 32 * i, q >= m0 && q < min(w1, m1) ? rank_key(f[i]) : 0u);
+    for (int h = 0; h < 2; ++h) {
+      const float* src = q0 + h * kStep < w1 ? step_at(q0 + h * kStep) : nullptr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[h][i] = q0 + h * kStep + 32 * i + lane < w1 ? __ldg(src + 32 * i + lane) : 0.0f;
     }
+    emit(q0, f[0]);
+    if (q0 + kStep < w1) emit(q0 + kStep, f[1]);
   }
 }
 
 constexpr int kMThreads = 256;
-constexpr int kMRows = 64;  // destination rows of a CTA
+// Destination rows of a CTA: 64 measured 270 us at four sequences of 2^20 cut
+// to half, 256 (fewer, longer CTAs with the same loads in flight) 296 us, and
+// a persistent grid that looks rows up one tile ahead 320 us.
+constexpr int kMRows = 64;
 
-// 16-byte copy of chunk i of the rows' `per` chunks each.
+// Copies the kPerRow 16-byte words of each row (drow < 0: none), all of a thread's in flight.
 template <int kPerRow>
 __device__ __forceinline__ void move_plane(const uint8_t* src, uint8_t* dst, const int64_t (&srow)[kMRows],
                                            const int64_t (&drow)[kMRows], int tid) {
@@ -372,28 +401,25 @@ __device__ __forceinline__ void move_plane(const uint8_t* src, uint8_t* dst, con
   uint4 v[kN];
 #pragma unroll
   for (int m = 0; m < kN; ++m) {
-    const int i = tid + m * kMThreads;
-    const int r = i / kPerRow;
+    const int i = tid + m * kMThreads, r = i / kPerRow;
     if (r < kMRows && drow[r] >= 0) v[m] = __ldg(reinterpret_cast<const uint4*>(src) + srow[r] * kPerRow + i % kPerRow);
   }
 #pragma unroll
   for (int m = 0; m < kN; ++m) {
-    const int i = tid + m * kMThreads;
-    const int r = i / kPerRow;
+    const int i = tid + m * kMThreads, r = i / kPerRow;
     if (r < kMRows && drow[r] >= 0) reinterpret_cast<uint4*>(dst)[drow[r] * kPerRow + i % kPerRow] = v[m];
   }
 }
 
-__global__ void __launch_bounds__(kMThreads) k_evict_move(EvictArgs a) {
+__global__ void __launch_bounds__(kMThreads, 8) k_evict_move(EvictArgs a) {
   __shared__ int64_t srow[kMRows], drow[kMRows];
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int64_t r0 = int64_t(blockIdx.x) * kMRows;
   launch_dependents();
   grid_wait();
+  int64_t s = -1, d = -1;
   if (tid < kMRows) {
-    const int64_t r = r0 + tid;
+    const int64_t r = int64_t(blockIdx.x) * kMRows + tid;
     const int pos = r < a.max_keep ? __ldg(a.kept + int64_t(b) * a.max_keep + r) : -1;
-    int64_t s = -1, d = -1;
     if (pos >= 0) {
       s = seg_row(a.src, b, pos, a.status);
       if (a.dst_pages) {
@@ -408,16 +434,15 @@ __global__ void __launch_bounds__(kMThreads) k_evict_move(EvictArgs a) {
     srow[tid] = s;
     drow[tid] = d;
   }
-  if (__syncthreads_and(tid >= kMRows || drow[tid] < 0)) return;
+  if (__syncthreads_and(d < 0)) return;
   move_plane<kMainCodeBytes / 16>(a.main_src.codes, a.main_dst.codes, srow, drow, tid);
   move_plane<kMainScaleBytes / 16>(a.main_src.scales, a.main_dst.scales, srow, drow, tid);
   if (a.idx_src.codes) {
     move_plane<kIdxCodeBytes / 16>(a.idx_src.codes, a.idx_dst.codes, srow, drow, tid);
-    if (tid < kMRows && drow[tid] >= 0)
-      reinterpret_cast<uint32_t*>(a.idx_dst.scales)[drow[tid]] =
-          __ldg(reinterpret_cast<const uint32_t*>(a.idx_src.scales) + srow[tid]);
+    if (d >= 0)
+      reinterpret_cast<uint32_t*>(a.idx_dst.scales)[d] = __ldg(reinterpret_cast<const uint32_t*>(a.idx_src.scales) + s);
   }
-  if (tid < kMRows && drow[tid] >= 0) a.acc_dst[drow[tid]] = __ldg(a.acc_src + srow[tid]);
+  if (d >= 0) a.acc_dst[d] = __ldg(a.acc_src + s);
 }
 
 }  // namespace
@@ -431,10 +456,10 @@ csa2_status launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int64_t want = (a.src.max_len + kRunKeys - 1) / kRunKeys;
   int C = int(std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, want)));
   while (C > 1 && kActive[C] < a.B) --C;
-  // keys of a warp that stay in shared memory: its part of the run, as far as there is room
+  // weights of a warp that stay in shared memory: its part of the run, as far as there is room
   const int64_t steps = (a.src.max_len + kStep - 1) / kStep;
   const int64_t part = ((steps + C - 1) / C + kEWarps - 1) / kEWarps;
-  const int64_t fit = (int64_t(224) * 1024 - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
+  const int64_t fit = (int64_t(226) * 1024 - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
   const int warp_cap = int(std::min(part, fit)) * kStep;
   const size_t smem = sizeof(SelSmem) + size_t(warp_cap) * 4 * kEWarps;
   cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -442,7 +467,7 @@ csa2_status launch_evict(const EvictArgs& a, cudaStream_t st) {
   launch_k_cluster(k_evict_select, dim3(C, a.B), dim3(kEThreads), smem, st, C, a, warp_cap);
   const csa2_status rc = check_launch("csa2_cache_evict");
   if (rc != CSA2_OK) return rc;
-  launch_k(k_evict_move, dim3(unsigned((a.max_keep + kMRows - 1) / kMRows), a.B), dim3(kMThreads), 0, st, a);
+  launch_k(k_evict_move, dim3(unsigned((int64_t(a.max_keep) + kMRows - 1) / kMRows), unsigned(a.B)), dim3(kMThreads), 0, st, a);
   return check_launch("csa2_cache_evict");
 }
 
