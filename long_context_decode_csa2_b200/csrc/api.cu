@@ -883,6 +883,7 @@ csa2_status weights_args(const char* fn, const csa2_mxfp4_cache& main_kv, int B,
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad B, Q or k");
   if (Q > 0 && (B == 0 || !cache_ok(main_kv)))
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad main cache, or queries without sequences");
+  if (main_kv.rows > INT32_MAX) return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": more than 2^31 cache rows");
   return CSA2_OK;
 }
 
