@@ -7,18 +7,19 @@
 // logits are needed again, not the values: the kernel reads the selected
 // rows, multiplies and adds.
 //
-// k_weights.  A warp takes groups of 16 selected rows of one query; the CTA's
-// four warps share the query, converted once, and nothing else: each streams
-// its own groups, cp.async bringing the next group's 272-byte rows while it
-// multiplies (no barrier after the first).  The product is 16 rows x 16 heads
-// (mma m16n8k16, fp32 accumulation): E2M1 codes are exact in fp16, each
-// block's E8M0 scale multiplies the block's fp32 sum, and a head's query row
-// is scaled by a power of two into [2^14, 2^15) at its largest element before
-// it becomes fp16, so every bf16 query element down to 2^-39 of the row's
-// largest is exact and no input leaves the fp16 range.  Inside a block the
-// order of the 32 dims is permuted (the same way for both operands) so that a
-// lane's 8 dims are one 32-bit word of codes.  Bound by instructions: about
-// 50 per row and warp, half of them to convert codes and apply scales.
+// k_weights.  A warp takes groups of 16 or 32 selected rows of one query; the
+// CTA's four warps share the query, converted once, and nothing else: each
+// streams its own groups, cp.async bringing the next group's 272-byte rows
+// while it works on this one (no barrier after the first).  The product is 16
+// rows x 16 heads (mma m16n8k16, fp32 accumulation): E2M1 codes are exact in
+// fp16, each block's E8M0 scale (converted once per group, in shared memory)
+// multiplies the block's fp32 sum, and a head's query row is scaled by a power
+// of two into [2^14, 2^15) at its largest element before it becomes fp16, so
+// every bf16 query element down to 2^-39 of the row's largest is exact and no
+// input leaves the fp16 range.  Inside a block the order of the 32 dims is
+// permuted (the same way for both operands) so that a lane's 8 dims are one
+// 32-bit word of codes.  Few rows: bound by the chain of dependent loads
+// (offsets, ids, rows).  Many: by instructions and shared memory reads.
 //
 // Order of the sums.  Entries are added in fp32 (weights of one query are at
 // most 16, sums grow over a sequence's life).  Where one query of a sequence
@@ -40,36 +41,53 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarps = 4;                     // per CTA; they share the query
-constexpr int kWThreads = 32 * kWarps;
-constexpr int kWRows = 16;                    // selected rows of a warp's group (MMA M)
-constexpr int kWStages = 2;
 constexpr int kRow = kMainCodeBytes + kMainScaleBytes;  // 272 bytes: codes, then scales
 constexpr int kQStride = kD + 32;             // halves: rows g and g+1 lie 4 of 8 16-byte columns apart
+constexpr int kBlocks = kD / 32;              // 16 scale blocks
 constexpr uint32_t kBig = 224;                // scale bytes from here on take the slow path (2^97 and more)
 
+// kTiles: MMA tiles (16 rows) of a warp's group.  Two tiles halve the shared
+// memory reads of the query, which bound the kernel next to the instructions
+// (48 sequences of up to 16 candidates, k = 2048: 97.6 us with one tile, 85.8
+// with two); one tile spreads few rows over more warps (64 queries of k = 512:
+// 8.5 against 9.5 us).
+template <int kTiles>
+struct Cfg {
+  static constexpr int kWarps = 4;                   // per CTA; they share the query
+  static constexpr int kStages = kTiles == 1 ? 2 : 1;      // groups of a warp in shared memory
+  static constexpr int kBlocksPerSm = kTiles == 1 ? 4 : 3;
+  static constexpr int kRows = 16 * kTiles;
+  static constexpr int kThreads = 32 * kWarps;
+};
+
+template <int kTiles>
 struct WSmem {
+  using C = Cfg<kTiles>;
   __half q[kHq][kQStride];
-  uint8_t raw[kWarps][kWStages][kWRows][kRow];
+  uint8_t raw[C::kWarps][C::kStages][C::kRows][kRow];
+  float scale[C::kWarps][C::kRows][kBlocks];  // the current group's block scales
   float qexp[kHq];                            // power of two that undoes the query row's scaling
   float lse[kHq];
 };
 
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tmov.b16 {t, _}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "h"(uint16_t(byte)));
-  return r;
+// Eight E2M1 codes (element 0 in the low nibble) -> four f16x2, exact.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&f)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+      : "r"(w));
 }
 // d = a b (from zero) and d += a b.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -119,52 +137,55 @@ __device__ __forceinline__ QueryRef query_ref(const WeightArgs& a, int i, int la
   return r;
 }
 
-// Scale byte j of word w as 2^(byte - 127 - sub).  Plain rows (no byte of kBig
-// or more) have sub = 0; a byte of 0 stands on blocks of zeros there, and 0.0
-// serves them.
-template <bool kPlain>
-__device__ __forceinline__ float e8m0(uint32_t w, int j, int sub) {
-  const int bits = int((j == 3 ? w >> 1 : w << (23 - 8 * j)) & 0x7F800000u);
-  return __int_as_float(kPlain ? bits : max(bits - (sub << 23), 0x00400000));
-}
-
-// Products of the warp's 16 rows with the 16 heads: acc[h][0..1] row g, heads
-// 8h + 2t and + 1; acc[h][2..3] row g + 8 (lane = 4 g + t).
-template <bool kPlain>
-__device__ __forceinline__ void products(const WSmem& sm, const uint8_t (&raw)[kWRows][kRow], float (&acc)[2][4],
-                                         int sub0, int sub1, int g, int t) {
-#pragma unroll 1
-  for (int j4 = 0; j4 < kD / 128; ++j4) {
-    const uint32_t sw0 = *reinterpret_cast<const uint32_t*>(raw[g] + kMainCodeBytes + 4 * j4);
-    const uint32_t sw1 = *reinterpret_cast<const uint32_t*>(raw[g + 8] + kMainCodeBytes + 4 * j4);
+// Products of the warp's rows with the 16 heads: acc[m][h][0..1] row 16m + g,
+// heads 8h + 2t and + 1; acc[m][h][2..3] row 16m + g + 8 (lane = 4 g + t).
+template <int kTiles>
+__device__ __forceinline__ void products(const __half (&qs)[kHq][kQStride], const uint8_t (&raw)[16 * kTiles][kRow],
+                                         const float (&scale)[16 * kTiles][kBlocks], float (&acc)[kTiles][2][4], int g,
+                                         int t) {
+#pragma unroll
+  for (int j4 = 0; j4 < kBlocks / 4; ++j4) {
+    float s[kTiles][2][4];
+#pragma unroll
+    for (int m = 0; m < 2 * kTiles; ++m) {
+      const float4 v = *reinterpret_cast<const float4*>(&scale[8 * m + g][4 * j4]);
+      s[m / 2][m & 1][0] = v.x, s[m / 2][m & 1][1] = v.y, s[m / 2][m & 1][2] = v.z, s[m / 2][m & 1][3] = v.w;
+    }
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int j = 4 * j4 + jj;
-      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(raw[g] + 16 * j + 4 * t);
-      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(raw[g + 8] + 16 * j + 4 * t);
-      const uint32_t a0[4] = {e2m1x2_f16x2(w0 & 255u), e2m1x2_f16x2(w1 & 255u), e2m1x2_f16x2((w0 >> 8) & 255u),
-                              e2m1x2_f16x2((w1 >> 8) & 255u)};
-      const uint32_t a1[4] = {e2m1x2_f16x2((w0 >> 16) & 255u), e2m1x2_f16x2((w1 >> 16) & 255u), e2m1x2_f16x2(w0 >> 24),
-                              e2m1x2_f16x2(w1 >> 24)};
-      const float s0 = e8m0<kPlain>(sw0, jj, sub0), s1 = e8m0<kPlain>(sw1, jj, sub1);
+      uint32_t a0[kTiles][4], a1[kTiles][4];
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) {
+        uint32_t f0[4], f1[4];
+        e2m1x8_f16(*reinterpret_cast<const uint32_t*>(raw[16 * m + g] + 16 * j + 4 * t), f0);
+        e2m1x8_f16(*reinterpret_cast<const uint32_t*>(raw[16 * m + g + 8] + 16 * j + 4 * t), f1);
+        a0[m][0] = f0[0], a0[m][1] = f1[0], a0[m][2] = f0[1], a0[m][3] = f1[1];
+        a1[m][0] = f0[2], a1[m][1] = f1[2], a1[m][2] = f0[3], a1[m][3] = f1[3];
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 q = *reinterpret_cast<const uint4*>(&sm.q[8 * h + g][32 * j + 8 * t]);
-        float d[4];
-        mma_f16_first(d, a0, q.x, q.y);
-        mma_f16(d, a1, q.z, q.w);
-        acc[h][0] = fmaf(d[0], s0, acc[h][0]);
-        acc[h][1] = fmaf(d[1], s0, acc[h][1]);
-        acc[h][2] = fmaf(d[2], s1, acc[h][2]);
-        acc[h][3] = fmaf(d[3], s1, acc[h][3]);
+        const uint4 q = *reinterpret_cast<const uint4*>(&qs[8 * h + g][32 * j + 8 * t]);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          float d[4];
+          mma_f16_first(d, a0[m], q.x, q.y);
+          mma_f16(d, a1[m], q.z, q.w);
+          acc[m][h][0] = fmaf(d[0], s[m][0][jj], acc[m][h][0]);
+          acc[m][h][1] = fmaf(d[1], s[m][0][jj], acc[m][h][1]);
+          acc[m][h][2] = fmaf(d[2], s[m][1][jj], acc[m][h][2]);
+          acc[m][h][3] = fmaf(d[3], s[m][1][jj], acc[m][h][3]);
+        }
       }
     }
   }
 }
 
-__global__ void __launch_bounds__(kWThreads) k_weights(WeightArgs a) {
+template <int kTiles>
+__global__ void __launch_bounds__(Cfg<kTiles>::kThreads, Cfg<kTiles>::kBlocksPerSm) k_weights(WeightArgs a) {
+  constexpr int kWarps = Cfg<kTiles>::kWarps, kWRows = Cfg<kTiles>::kRows, kStages = Cfg<kTiles>::kStages;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  WSmem& sm = *reinterpret_cast<WSmem*>(smem_raw);
+  WSmem<kTiles>& sm = *reinterpret_cast<WSmem<kTiles>*>(smem_raw);
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int groups = (a.k + kWRows - 1) / kWRows, stride = gridDim.y * kWarps;
@@ -173,7 +194,7 @@ __global__ void __launch_bounds__(kWThreads) k_weights(WeightArgs a) {
   int grp = blockIdx.y * kWarps + warp;
   launch_dependents();
   grid_wait();
-  // ids of a group (lanes 0 .. 15); a group behind the last has none
+  // ids of a group, one per lane; a group behind the last has none
   auto load_ids = [&](int gr) {
     const int slot = gr * kWRows + lane;
     return lane < kWRows && slot < a.k ? __ldg(ids + slot) : -1;
@@ -248,64 +269,76 @@ __global__ void __launch_bounds__(kWThreads) k_weights(WeightArgs a) {
   for (int h = 0; h < 4; ++h) {
     lse[h] = sm.lse[8 * (h >> 1) + 2 * t + (h & 1)];
     qexp[h] = sm.qexp[8 * (h >> 1) + 2 * t + (h & 1)];
+    if (lse[h] == -INFINITY) lse[h] = INFINITY;  // no key at all: nothing has a weight
   }
-  for (int stage = 0; grp < groups; grp += stride, stage ^= 1) {
+  for (int stage = 0; grp < groups; grp += stride, stage = (stage + 1) % kStages) {
     const int next = row_of(id);
-    if (grp + stride < groups) {
+    if (kStages > 1 && grp + stride < groups) {
       issue(stage ^ 1, next);
       id = load_ids(grp + 2 * stride);
       sm100::cp_async_wait<1>();
     } else {
+      id = load_ids(grp + 2 * stride);
       sm100::cp_async_wait<0>();
     }
     __syncwarp();
     const uint8_t(&raw)[kWRows][kRow] = sm.raw[warp][stage];
-    // rows with a scale byte of kBig or more: lane (g, t) looks at word t of rows g and g + 8
-    const uint32_t b0 = *reinterpret_cast<const uint32_t*>(raw[g] + kMainCodeBytes + 4 * t);
-    const uint32_t b1 = *reinterpret_cast<const uint32_t*>(raw[g + 8] + kMainCodeBytes + 4 * t);
-    const uint32_t big0 = b0 & (b0 << 1) & (b0 << 2) & 0x80808080u, big1 = b1 & (b1 << 1) & (b1 << 2) & 0x80808080u;
-    static_assert(kBig == 0xE0, "the three top bits");
-    float acc[2][4] = {}, mul0 = 1.0f, mul1 = 1.0f;
-    if (!__any_sync(0xffffffffu, big0 | big1)) {
-      products<true>(sm, raw, acc, 0, 0, g, t);
-    } else {
-      // Such a row is multiplied with its scales 2^64 times smaller (blocks
-      // that this takes below 2^-127 do not matter beside one of 2^97), and
-      // one with an E8M0 NaN becomes NaN.
-      auto row_any = [&](bool v) { return ((__ballot_sync(0xffffffffu, v) >> (4 * g)) & 15u) != 0u; };
-      auto has_nan = [&](uint32_t w) { return (w & 255u) == 255u || (w >> 8 & 255u) == 255u || (w >> 16 & 255u) == 255u || w >> 24 == 255u; };
-      const bool r0 = row_any(big0 != 0u), r1 = row_any(big1 != 0u), n0 = row_any(has_nan(b0)), n1 = row_any(has_nan(b1));
-      products<false>(sm, raw, acc, r0 ? 64 : 0, r1 ? 64 : 0, g, t);
-      mul0 = n0 ? __uint_as_float(0x7FC00000u) : r0 ? 1.8446744073709552e19f : 1.0f;  // 2^64
-      mul1 = n1 ? __uint_as_float(0x7FC00000u) : r1 ? 1.8446744073709552e19f : 1.0f;
+    // ---- block scales as floats: lane (g, t) does words t of rows g, g + 8, .. ----
+    float mul[2 * kTiles];
+    uint32_t word[2 * kTiles], big[2 * kTiles], any = 0;
+#pragma unroll
+    for (int m = 0; m < 2 * kTiles; ++m) {
+      word[m] = *reinterpret_cast<const uint32_t*>(raw[8 * m + g] + kMainCodeBytes + 4 * t);
+      static_assert(kBig == 0xE0, "the three top bits");
+      big[m] = word[m] & (word[m] << 1) & (word[m] << 2) & 0x80808080u;  // scale bytes of kBig or more
+      any |= big[m];
+      mul[m] = 1.0f;
     }
+    const bool slow = __any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int m = 0; m < 2 * kTiles; ++m) {
+      int sub = 0;
+      // A row with such a byte is multiplied with its scales 2^64 times smaller
+      // (blocks that this takes below 2^-127 do not matter beside one of 2^97).
+      if (slow && (__ballot_sync(0xffffffffu, big[m] != 0u) >> (4 * g) & 15u) != 0u)
+        sub = 64 << 23, mul[m] = 1.8446744073709552e19f;  // 2^64
+      // 2^(byte - 127 - sub); 255 is E8M0's NaN
+      auto e8m0 = [&](uint32_t byte) {
+        const float v = __int_as_float(max(int(byte << 23) - sub, 0x00400000));
+        return slow && byte == 255u ? __uint_as_float(0x7FC00000u) : v;
+      };
+      *reinterpret_cast<float4*>(&sm.scale[warp][8 * m + g][4 * t]) =
+          make_float4(e8m0(word[m] & 255u), e8m0(word[m] >> 8 & 255u), e8m0(word[m] >> 16 & 255u), e8m0(word[m] >> 24));
+    }
+    __syncwarp();
+    float acc[kTiles][2][4] = {};
+    products<kTiles>(sm.q, raw, sm.scale[warp], acc, g, t);
+    __syncwarp();  // this stage is read before its next copies
+    const int here = row;
+    if (kStages == 1 && grp + stride < groups) issue(0, next);
+    row = next;
     // ---- weights: exp(logit - lse), summed over the heads (four here, the others in lanes of other t) ----
-    float w0 = 0.0f, w1 = 0.0f;
+    float w[2 * kTiles];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      // (no key at all: lse is -inf, and nothing has a weight)
-      const bool none = lse[h] == -INFINITY;
-      const float x0 = fmaf(acc[h >> 1][h & 1] * qexp[h] * mul0, a.sm_scale, -lse[h]);
-      const float x1 = fmaf(acc[h >> 1][2 + (h & 1)] * qexp[h] * mul1, a.sm_scale, -lse[h]);
-      w0 += none ? 0.0f : expf(x0);
-      w1 += none ? 0.0f : expf(x1);
-    }
+    for (int m = 0; m < 2 * kTiles; ++m) {
+      w[m] = 0.0f;
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      w0 += __shfl_xor_sync(0xffffffffu, w0, d);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, d);
+      for (int h = 0; h < 4; ++h)
+        w[m] += expf(fmaf(acc[m >> 1][h >> 1][2 * (m & 1) + (h & 1)] * qexp[h] * mul[m], a.sm_scale, -lse[h]));
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) w[m] += __shfl_xor_sync(0xffffffffu, w[m], d);
     }
-    // lane (g, 0) has row g, lane (g, 1) row g + 8
-    const int r = g + 8 * (t & 1), at = __shfl_sync(0xffffffffu, row, r);
-    if (t < 2) {
-      float v = at >= 0 ? (t ? w1 : w0) : 0.0f;
-      if (v < 1.17549435e-38f) v = 0.0f;  // 2^-126: the fp32 atomics below flush subnormal numbers
+    // lane (g, t) has row g + 8 t
+    const int r = g + 8 * t, at = __shfl_sync(0xffffffffu, here, r % kWRows);
+    if (r < kWRows) {
+      float v = t == 0 ? w[0] : w[1];
+      if (kTiles == 2 && t >= 2) v = t == 2 ? w[2 * kTiles - 2] : w[2 * kTiles - 1];
+      // 2^-126: the fp32 atomics below flush subnormal numbers
+      if (at < 0 || v < 1.17549435e-38f) v = 0.0f;
       const int slot = grp * kWRows + r;
       if (slot < a.k) wout[slot] = v;
       if (at >= 0 && !ref.several) atomicAdd(a.acc + at, v);
     }
-    row = next;
-    __syncwarp();  // this stage is read before its next copies
   }
 }
 
@@ -327,48 +360,62 @@ __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
   if (most <= 0) return;
   const int64_t len = seg_len_checked(a.sd, b, nullptr);
   const int lo = int(len * blockIdx.y / gridDim.y), hi = int(len * (blockIdx.y + 1) / gridDim.y);
-  // this thread's slots of query i that lie in this part: ids, then weights
-  auto fetch = [&](int i, int (&id)[kAPer], float (&w)[kAPer]) {
-    const int64_t at = int64_t(i) * a.k;
+  // This thread's slots of a query: its ids are fetched two queries ahead, the
+  // weights of those that lie in this part one ahead.
+  auto fetch_ids = [&](int i, int (&id)[kAPer]) {
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
       const int j = tid + m * kAThreads;
-      id[m] = j < a.k ? __ldg(a.topk + at + j) : -1;
+      id[m] = i <= q0 + most && j < a.k ? __ldg(a.topk + int64_t(i) * a.k + j) : -1;
     }
+  };
+  auto fetch_weights = [&](int i, int (&id)[kAPer], float (&w)[kAPer]) {
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
       if (id[m] < lo || id[m] >= hi) id[m] = -1;
-      w[m] = id[m] >= 0 ? __ldcg(a.weights + at + tid + m * kAThreads) : 0.0f;
+      w[m] = id[m] >= 0 ? __ldcg(a.weights + int64_t(i) * a.k + tid + m * kAThreads) : 0.0f;
     }
   };
-  int id[kAPer], id2[kAPer];
-  float w[kAPer], w2[kAPer];
-  fetch(q0, id, w);
+  int id[kAPer], id1[kAPer], id2[kAPer];
+  float w[kAPer], w1[kAPer];
+  fetch_ids(q0, id);
+  fetch_ids(q0 + 1, id1);
+  fetch_weights(q0, id, w);
   for (int i = q0; i <= q0 + most; ++i) {
-    if (i < q0 + most) fetch(i + 1, id2, w2);
+    fetch_ids(i + 2, id2);
+    fetch_weights(i + 1, id1, w1);
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
       if (id[m] >= 0) {
         const int64_t row = entry_row(a.sd, b, id[m], nullptr);
         if (row >= 0) atomicAdd(a.acc + row, w[m]);
       }
-      id[m] = id2[m];
-      w[m] = w2[m];
+      id[m] = id1[m];
+      w[m] = w1[m];
+      id1[m] = id2[m];
     }
     __syncthreads();
   }
 }
 
+template <int kTiles>
+void launch_tiles(const WeightArgs& a, int64_t ctas, cudaStream_t st) {
+  constexpr int kSlots = Cfg<kTiles>::kRows * Cfg<kTiles>::kWarps;  // of a CTA at a time
+  const int most = (a.k + kSlots - 1) / kSlots;
+  const int S = int(std::max<int64_t>(1, std::min<int64_t>(most, (ctas + a.Q - 1) / a.Q)));
+  cudaFuncSetAttribute(k_weights<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(WSmem<kTiles>)));
+  launch_k(k_weights<kTiles>, dim3(a.Q, S), dim3(Cfg<kTiles>::kThreads), sizeof(WSmem<kTiles>), st, a);
+}
+
 }  // namespace
 
 void launch_weights(const WeightArgs& a, cudaStream_t st) {
-  // CTAs per query: one for every 64 slots while the SMs have room for all of
-  // them, else enough for a few waves of four CTAs per SM
-  const int most = (a.k + kWRows * kWarps - 1) / (kWRows * kWarps);
-  const int64_t room = 16 * int64_t(num_sms());
-  const int S = int(std::max<int64_t>(1, std::min<int64_t>(most, (room + a.Q - 1) / a.Q)));
-  cudaFuncSetAttribute(k_weights, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(WSmem)));
-  launch_k(k_weights, dim3(a.Q, S), dim3(kWThreads), sizeof(WSmem), st, a);
+  // Two tiles per warp once there are more than 32 tiles per SM.  CTAs of a
+  // query: as many as its slots allow while the grid stays at 16 (one tile)
+  // or 4 (two) CTAs per SM, about a wave of those that run together.
+  const int64_t tiles = int64_t(a.Q) * ((a.k + 15) / 16), sms = num_sms();
+  if (tiles <= 32 * sms) launch_tiles<1>(a, 16 * sms, st);
+  else launch_tiles<2>(a, 4 * sms, st);
   if (!a.q_off) return;
   // parts of a sequence: the ids are read by each of them
   const int P = int(std::max<int64_t>(1, std::min<int64_t>(16, 4 * int64_t(num_sms()) / a.B)));
