@@ -496,19 +496,25 @@ def _launch(fn, tensors, stream, *args):
     necessarily the current one); stream None is that device's current stream."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise Csa2Error(-1, fn, f"tensors on {dev} and {t.device}")
+        if t is not None:
+            d = t.get_device()  # (-1: a host tensor)
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise Csa2Error(-1, fn, f"tensors on devices {dev} and {d}")
     f = getattr(lib(), fn)
-    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = f(*args, _stream(stream))
-    else:
+    if dev is None or dev < 0:
         rc = f(*args, _stream(stream))
-    _check(rc, fn)
+    else:
+        # (the raw handle: torch.cuda.current_stream() builds a Stream object, 3.7 us)
+        st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                rc = f(*args, st)
+        else:
+            rc = f(*args, st)
+    if rc != 0:
+        _check(rc, fn)
 
 
 def _cache_tensors(*caches):
@@ -523,11 +529,12 @@ def _prob_rows(fn, name, t, Q, V):
     contiguous, rows any distance apart."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _PROB_TYPES:
         raise Csa2Error(-1, fn, f"{name}: a 2-d fp32, bf16 or fp16 tensor expected")
-    if t.shape[0] < Q or t.shape[1] != V:
-        raise Csa2Error(-1, fn, f"{name}: [{Q}, {V}] expected, got {list(t.shape)}")
+    rows, cols = t.shape
+    if rows < Q or cols != V:
+        raise Csa2Error(-1, fn, f"{name}: [{Q}, {V}] expected, got [{rows}, {cols}]")
     if V > 1 and t.stride(1) != 1:
         raise Csa2Error(-1, fn, f"{name}: the probabilities of a row must be contiguous")
-    return _arg(fn, name, t[:1, :1], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
+    return _arg(fn, name, t if t.is_contiguous() else t[0], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
 
 
 def csa2_verify_drafts_workspace_bytes(B, V):

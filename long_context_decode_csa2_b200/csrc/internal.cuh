@@ -257,7 +257,7 @@ void launch_compress(const CompressArgs& a, cudaStream_t st);
 
 // Verification of drafted tokens: per sequence the accepted prefix of its
 // candidates and the next token.
-constexpr int kVerifySegment = 1024;  // vocabulary entries of one partial sum
+constexpr int kVerifySegment = 256;   // vocabulary entries of one partial sum
 struct VerifyArgs {
   const void* target;      // [Q] rows of V, CSA2_TYPE_* elements
   int target_type;

@@ -16,11 +16,12 @@
 // r C_V about once in a hundred draws, in fp64 about once in 10^11.
 //
 // Work split.  Only the stop row of a sequence is read (n - 1 tests read
-// single elements), by S CTAs: a warp sums segments of 1024 elements and
-// leaves one fp64 sum per segment in the workspace; the last CTA of the
-// sequence to finish scans them, and one of its warps reads the segment that
-// holds r C_V again (from L2) to find the token.  The sums do not depend on
-// S or on the order of arrival.
+// single elements), by S CTAs, all sequences' at once: a warp takes a segment
+// of 256 elements at a time and leaves its fp64 sum in the workspace; the last CTA of the sequence to finish
+// scans them, and one of its warps reads the segment that holds r C_V again
+// (from L2) to find the token.  The sums do not depend on S or on the order
+// of arrival.  Bound by the chain of dependent steps (tests 2 us, arrival
+// 1 us, scan and second read 3 us) until the rows are tens of MB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,9 +37,9 @@ namespace {
 constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVec = 8;                       // consecutive elements per lane and step
-constexpr int kSeg = kVerifySegment;          // elements of one partial sum
-constexpr int kSteps = kSeg / (32 * kVec);    // 4
-static_assert(kSeg == kSteps * 32 * kVec, "a segment is a whole number of warp steps");
+constexpr int kSeg = kVerifySegment;          // elements of one partial sum: 8 per lane
+constexpr int kFly = 1;                       // segments of a warp whose loads are in flight together (32 warps per SM)
+static_assert(kSeg == 32 * kVec, "a segment is one vector per lane");
 
 struct NoDraft {};  // drafts without probabilities
 
@@ -49,20 +50,26 @@ __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 // A probability that is negative or NaN counts as 0.
 __device__ __forceinline__ float prob(float x) { return x > 0.0f ? x : 0.0f; }
 
-// Elements e .. e+7 of a row of V elements (0 behind its end).  Rows start at
-// any multiple of their element size: a vector that lies inside the row is
-// read as the aligned 16-byte words that cover it, shifted into place; one at
-// an edge, where those words would leave the row, element by element.
+// Eight consecutive elements of a row as they lie in memory.  Rows start at
+// any multiple of their element size: the vector is read as the aligned
+// 16-byte words that cover it (one more than it fills where it is not aligned
+// itself) and shifted into place.
 template <class T>
-__device__ __forceinline__ void load8(const T* row, int64_t e, int64_t V, float (&x)[kVec]) {
-  constexpr int kWords = kVec * int(sizeof(T)) / 4;  // 32-bit words of the vector
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + e);
-  const int mis = int(at & 15);
-  const int64_t pad = mis / int(sizeof(T));           // elements of the first word before e
-  const int64_t tail = mis ? 16 / int(sizeof(T)) - pad : 0;
-  if (e - pad >= 0 && e + kVec + tail <= V) {
-    const uint4* g = reinterpret_cast<const uint4*>(at - mis);
-    uint32_t w[kWords + 4];
+struct Raw8 {
+  static constexpr int kWords = kVec * int(sizeof(T)) / 4;  // 32-bit words of the vector
+  uint32_t w[kWords + 4];
+
+  // Elements of row that the covering words take from before e and behind e+7.
+  static __device__ __forceinline__ int misalignment(const T* at) {
+    return int(reinterpret_cast<uintptr_t>(at) & 15);
+  }
+  static __device__ __forceinline__ bool inside(const T* row, int64_t e, int64_t n, int64_t V) {
+    const int mis = misalignment(row + e);
+    const int pad = mis / int(sizeof(T)), tail = mis ? 16 / int(sizeof(T)) - pad : 0;
+    return e - pad >= 0 && e + n + tail <= V;
+  }
+  __device__ __forceinline__ void load(const T* at, int mis) {
+    const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) - mis);
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
       const uint4 v = __ldg(g + i);
@@ -71,6 +78,10 @@ __device__ __forceinline__ void load8(const T* row, int64_t e, int64_t V, float 
     if (mis) {
       const uint4 v = __ldg(g + kWords / 4);
       w[kWords] = v.x, w[kWords + 1] = v.y, w[kWords + 2] = v.z, w[kWords + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void unpack(int mis, float (&x)[kVec]) {
+    if (mis) {
       if (mis & 8) {
 #pragma unroll
         for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
@@ -93,41 +104,80 @@ __device__ __forceinline__ void load8(const T* row, int64_t e, int64_t V, float 
         x[i] = as_float(*reinterpret_cast<const T*>(&h));
       }
     }
-  } else {
+  }
+};
+
+// Elements e .. e+7 of a row (0 behind its end), one by one.
+template <class T>
+__device__ __forceinline__ void load8_edge(const T* row, int64_t e, int64_t V, float (&x)[kVec]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = e + i < V ? as_float(row[e + i]) : 0.0f;
+  for (int i = 0; i < kVec; ++i) x[i] = e + i < V ? as_float(row[e + i]) : 0.0f;
+}
+
+// What the next token is drawn from: p where every draft stood or the
+// residual is empty, else max(p - q, 0).
+template <class TQ>
+struct StopRow {
+  const TQ* q;      // draft row (null: p itself)
+  int drafted;      // drafts without probabilities: the rejected token (-1: p itself)
+};
+
+// Weight of element e from its probabilities.
+template <class TQ>
+__device__ __forceinline__ double weight_of(float x, float y, const StopRow<TQ>& s, int64_t e) {
+  const float a = prob(x);
+  if constexpr (std::is_same<TQ, NoDraft>::value) {
+    return double(e == s.drafted ? prob(a - 1.0f) : a);  // the draft's distribution is 1 at its token
+  } else {
+    const float b = prob(y);  // (0 where there is no draft row)
+    return a > b ? double(a) - double(b) : 0.0;
   }
 }
 
-// The weights of elements e .. e+7 of the stop row: p where every draft stood
-// or the residual is empty (`plain`), else max(p - q, 0).
-template <class TQ>
-struct StopRow {
-  const TQ* q;      // draft row (null: plain)
-  int drafted;      // drafts without probabilities: the rejected token (-1: plain)
-};
-
-template <class TP, class TQ>
-__device__ __forceinline__ void weights8(const TP* p, const StopRow<TQ>& s, int64_t e, int64_t V, double (&w)[kVec]) {
-  float x[kVec];
-  load8(p, e, V, x);
-  if constexpr (std::is_same<TQ, NoDraft>::value) {
+// w[i]: this lane's 8 weights of segment seg + i, the loads of all kN segments
+// in flight together.  Segments at an edge, whose covering words would leave
+// the row (or that lie behind it), are read element by element.
+template <int kN, class TP, class TQ>
+__device__ __forceinline__ void segment_weights(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, int lane,
+                                                double (&w)[kN][kVec]) {
+  constexpr bool kDraft = !std::is_same<TQ, NoDraft>::value;
+  using QT = typename std::conditional<kDraft, TQ, float>::type;
+  const int64_t e0 = int64_t(seg) * kSeg;
+  const QT* q = nullptr;
+  if constexpr (kDraft) q = s.q;
+  if (Raw8<TP>::inside(p, e0, kN * kSeg, V) && (q == nullptr || Raw8<QT>::inside(q, e0, kN * kSeg, V))) {
+    const TP* pe = p + e0 + lane * kVec;
+    const QT* qe = q + e0 + lane * kVec;
+    const int pm = Raw8<TP>::misalignment(pe), qm = q ? Raw8<QT>::misalignment(qe) : 0;
+    Raw8<TP> pr[kN];
+    Raw8<QT> qr[kN];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      // the draft's distribution is 1 at its token
-      const float less = e + i == s.drafted ? prob(prob(x[i]) - 1.0f) : prob(x[i]);
-      w[i] = double(less);
+    for (int i = 0; i < kN; ++i) pr[i].load(pe + i * kSeg, pm);
+    if (kDraft && q != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) qr[i].load(qe + i * kSeg, qm);
     }
-  } else if (s.q == nullptr) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = double(prob(x[i]));
+    for (int i = 0; i < kN; ++i) {
+      float x[kVec], y[kVec] = {};
+      pr[i].unpack(pm, x);
+      if (kDraft && q != nullptr) qr[i].unpack(qm, y);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) w[i][j] = weight_of(x[j], y[j], s, e0 + i * kSeg + lane * kVec + j);
+    }
   } else {
-    float y[kVec];
-    load8(s.q, e, V, y);
+#pragma unroll 1
+    for (int i = 0; i < kN; ++i) {
+      float x[kVec], y[kVec] = {};
+      const int64_t e = e0 + i * kSeg + lane * kVec;
+      load8_edge(p, e, V, x);
+      if (kDraft && q != nullptr) load8_edge(q, e, V, y);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float a = prob(x[i]), b = prob(y[i]);
-      w[i] = a > b ? double(a) - double(b) : 0.0;
+      for (int m = 0; m < kN; ++m)
+        if (m == i) {
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) w[m][j] = weight_of(x[j], y[j], s, e + j);
+        }
     }
   }
 }
@@ -146,49 +196,47 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {  // inclusive
   return v;
 }
 
+// Sums of segments seg .. seg + kFly - 1 (those below nseg) to part.
 template <class TP, class TQ>
-__device__ __forceinline__ double segment_sum(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, int lane) {
-  double acc = 0.0;
+__device__ __forceinline__ void segment_sums(const TP* p, const StopRow<TQ>& s, int seg, int nseg, int64_t V, int lane,
+                                             double* part) {
+  double w[kFly][kVec], mine = 0.0;
+  segment_weights<kFly>(p, s, seg, V, lane, w);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    double w[kVec];
-    weights8(p, s, int64_t(seg) * kSeg + (i * 32 + lane) * kVec, V, w);
+  for (int i = 0; i < kFly; ++i) {
+    double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) acc += w[j];
+    for (int j = 0; j < kVec; ++j) sum += w[i][j];
+    sum = warp_sum(sum);
+    if (lane == i) mine = sum;
   }
-  return warp_sum(acc);
+  if (lane < kFly && seg + lane < nseg) __stcg(part + seg + lane, mine);
 }
 
 // The first token of segment `seg` whose running sum (from `base`) passes
 // `want`; where rounding lets none pass, the last one with a weight (-1: none).
 template <class TP, class TQ>
-__device__ int segment_find(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, double base, double want, int lane) {
-  int last = -1;
-  for (int i = 0; i < kSteps; ++i) {
-    const int64_t e = int64_t(seg) * kSeg + (i * 32 + lane) * kVec;
-    double w[kVec], sum = 0.0;
-    weights8(p, s, e, V, w);
+__device__ __forceinline__ int segment_find(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, double base,
+                                            double want, int lane) {
+  double w[1][kVec], sum = 0.0;
+  segment_weights<1>(p, s, seg, V, lane, w);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) sum += w[j];
-    const double incl = warp_scan(sum, lane);
-    double c = base + __shfl_up_sync(0xffffffffu, incl, 1);
-    if (lane == 0) c = base;
-    int hit = -1, here = -1;
+  for (int j = 0; j < kVec; ++j) sum += w[0][j];
+  const double incl = warp_scan(sum, lane);
+  double c = __shfl_up_sync(0xffffffffu, incl, 1);
+  c = base + (lane == 0 ? 0.0 : c);
+  int hit = -1, last = -1;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      c += w[j];
-      if (w[j] > 0.0) {
-        here = int(e) + j;
-        if (hit < 0 && c > want) hit = here;
-      }
+  for (int j = 0; j < kVec; ++j) {
+    c += w[0][j];
+    if (w[0][j] > 0.0) {
+      last = seg * kSeg + lane * kVec + j;
+      if (hit < 0 && c > want) hit = last;
     }
-    const unsigned any = __ballot_sync(0xffffffffu, hit >= 0);
-    if (any) return __shfl_sync(0xffffffffu, hit, __ffs(any) - 1);
-    const unsigned some = __ballot_sync(0xffffffffu, here >= 0);
-    if (some) last = __shfl_sync(0xffffffffu, here, 31 - __clz(some));
-    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return last;
+  const unsigned any = __ballot_sync(0xffffffffu, hit >= 0);
+  if (any) return __shfl_sync(0xffffffffu, hit, __ffs(any) - 1);
+  return __reduce_max_sync(0xffffffffu, last);
 }
 
 struct Shared {
@@ -201,16 +249,24 @@ struct Shared {
 // Scans the segment sums: the first segment whose running sum passes r C_V
 // (the last one with a weight where none does), what lies before it, and the
 // total.  Every thread of the CTA.
-__device__ void find_segment(const double* part, int nseg, float r, Shared& sm) {
+__device__ __forceinline__ void find_segment(const double* part, int nseg, float r, Shared& sm) {
+  constexpr int kKeep = 4;                             // sums of a thread in registers (vocabularies up to 2^18)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (nseg + kVThreads - 1) / kVThreads;  // consecutive segments of this thread
   const int s0 = min(nseg, tid * per), s1 = min(nseg, s0 + per);
-  double mine = 0.0;
+  double v[kKeep], mine = 0.0;
   int pos = -1;
-  for (int s = s0; s < s1; ++s) {
-    const double v = __ldcg(part + s);
-    mine += v;
-    if (v > 0.0) pos = s;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) v[k] = s0 + k < s1 ? __ldcg(part + s0 + k) : 0.0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    mine += v[k];
+    if (v[k] > 0.0) pos = s0 + k;
+  }
+  for (int s = s0 + kKeep; s < s1; ++s) {
+    const double x = __ldcg(part + s);
+    mine += x;
+    if (x > 0.0) pos = s;
   }
   const double incl = warp_scan(mine, lane);
   pos = __reduce_max_sync(0xffffffffu, pos);
@@ -229,23 +285,30 @@ __device__ void find_segment(const double* part, int nseg, float r, Shared& sm) 
   const double want = double(r) * total;
   double c = __shfl_up_sync(0xffffffffu, incl, 1);
   c = before + (lane == 0 ? 0.0 : c);
-  const double c0 = c;
+  // this thread's first segment that passes, and what lies before it (or
+  // before segment lastpos, which is taken where none passes)
   int hit = -1;
-  for (int s = s0; s < s1 && hit < 0; ++s) {
-    c += __ldcg(part + s);
-    if (c > want) hit = s;
-  }
+  double base = 0.0, base_last = 0.0;
+  auto step = [&](int s, double x) {
+    if (s == lastpos) base_last = c;
+    if (hit < 0 && c + x > want) hit = s, base = c;
+    c += x;
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (s0 + k < s1) step(s0 + k, v[k]);
+  for (int s = s0 + kKeep; s < s1; ++s) step(s, __ldcg(part + s));
   if (hit >= 0) atomicMin(&sm.seg, hit);
   __syncthreads();
-  const int seg = sm.seg == 0x7fffffff ? lastpos : sm.seg;
-  if (seg >= s0 && seg < s1) {
-    double b = c0;
-    for (int s = s0; s < seg; ++s) b += __ldcg(part + s);
-    sm.base = b;
-  }
+  const bool none = sm.seg == 0x7fffffff;
+  const int seg = none ? lastpos : sm.seg;
   __syncthreads();
-  if (tid == 0) {
+  if (none ? lastpos >= s0 && lastpos < s1 : hit == seg) {
+    sm.base = none ? base_last : base;
     sm.seg = seg;
+  }
+  if (tid == 0) {
+    if (none && lastpos < 0) sm.seg = -1;
     sm.total = total;
     sm.want = want;
   }
@@ -253,7 +316,7 @@ __device__ void find_segment(const double* part, int nseg, float r, Shared& sm) 
 }
 
 template <class TP, class TQ>
-__global__ void __launch_bounds__(kVThreads) k_verify(VerifyArgs a) {
+__global__ void __launch_bounds__(kVThreads, 4) k_verify(VerifyArgs a) {
   constexpr bool kDraft = !std::is_same<TQ, NoDraft>::value;
   using QT = typename std::conditional<kDraft, TQ, float>::type;
   __shared__ Shared sm;
@@ -330,18 +393,18 @@ __global__ void __launch_bounds__(kVThreads) k_verify(VerifyArgs a) {
   }
   const int nseg = (a.V + kSeg - 1) / kSeg;
   double* part = a.part + int64_t(b) * nseg;
-  for (int g = blockIdx.y * kVWarps + warp; g < nseg; g += gridDim.y * kVWarps) {
-    const double v = segment_sum(p, s, g, a.V, lane);
-    if (lane == 0) __stcg(part + g, v);
-  }
+  for (int g = (blockIdx.y * kVWarps + warp) * kFly; g < nseg; g += gridDim.y * kVWarps * kFly)
+    segment_sums(p, s, g, nseg, a.V, lane, part);
   __syncthreads();
-  if (tid == 0) {
-    int old;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counters + b) : "memory");
-    sm.last = old == int(gridDim.y) - 1;
+  if (gridDim.y > 1) {
+    if (tid == 0) {
+      int old;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counters + b) : "memory");
+      sm.last = old == int(gridDim.y) - 1;
+    }
+    __syncthreads();
+    if (!sm.last) return;
   }
-  __syncthreads();
-  if (!sm.last) return;
   // ---- the last CTA draws the token ----
   const float r = a.r[b];
   find_segment(part, nseg, r, sm);
@@ -350,10 +413,7 @@ __global__ void __launch_bounds__(kVThreads) k_verify(VerifyArgs a) {
     // CTA sums the row again; the test above fails on p = q only where u >= 1
     // or p(x) = 0, so this is rare)
     s = StopRow<TQ>{nullptr, -1};
-    for (int g = warp; g < nseg; g += kVWarps) {
-      const double v = segment_sum(p, s, g, a.V, lane);
-      if (lane == 0) __stcg(part + g, v);
-    }
+    for (int g = warp * kFly; g < nseg; g += kVWarps * kFly) segment_sums(p, s, g, nseg, a.V, lane, part);
     __syncthreads();
     find_segment(part, nseg, r, sm);
   }
@@ -392,11 +452,11 @@ void launch_target(const VerifyArgs& a, int S, cudaStream_t st) {
 }  // namespace
 
 void launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  // CTAs per sequence: a warp per segment while the batch leaves room, and
-  // about four CTAs per SM in all
+  // CTAs per sequence: as many as its segments keep busy, while those of all
+  // sequences run at once (four CTAs per SM): a second wave would repeat the
+  // tests' chain of loads (64 rows of 131072: 23.5 us in three waves)
   const int nseg = (a.V + kSeg - 1) / kSeg;
-  const int want = (4 * num_sms() + a.B - 1) / a.B;
-  const int S = std::max(1, std::min(want, (nseg + kVWarps - 1) / kVWarps));
+  const int S = std::max(1, std::min(4 * num_sms() / a.B, (nseg + kVWarps * kFly - 1) / (kVWarps * kFly)));
   switch (a.target_type) {
     case CSA2_TYPE_F32: return launch_target<float>(a, S, st);
     case CSA2_TYPE_BF16: return launch_target<__nv_bfloat16>(a, S, st);
