@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<kTiles>::kThreads, Cfg<kTiles>::kBlocksPer
 
 // Sequences of which several queries count: their weights are added query by
 // query.  CTA (p, b) owns positions [len p / P, len (p+1) / P) of sequence b.
-constexpr int kAThreads = 256;
+constexpr int kAThreads = 512;
 constexpr int kAPer = CSA2_MAX_TOPK / kAThreads;  // slots of a thread
 
 __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
   const int64_t len = seg_len_checked(a.sd, b, nullptr);
   const int lo = int(len * blockIdx.y / gridDim.y), hi = int(len * (blockIdx.y + 1) / gridDim.y);
   // This thread's slots of a query: its ids are fetched two queries ahead, the
-  // weights of those that lie in this part one ahead.
+  // cache rows and weights of those that lie in this part one ahead.
   auto fetch_ids = [&](int i, int (&id)[kAPer]) {
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
@@ -369,28 +369,27 @@ __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
       id[m] = i <= q0 + most && j < a.k ? __ldg(a.topk + int64_t(i) * a.k + j) : -1;
     }
   };
-  auto fetch_weights = [&](int i, int (&id)[kAPer], float (&w)[kAPer]) {
+  const int64_t base = a.sd.pages ? 0 : a.sd.row_off[b];
+  auto fetch_rows = [&](int i, const int (&id)[kAPer], int (&row)[kAPer], float (&w)[kAPer]) {
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
-      if (id[m] < lo || id[m] >= hi) id[m] = -1;
-      w[m] = id[m] >= 0 ? __ldcg(a.weights + int64_t(i) * a.k + tid + m * kAThreads) : 0.0f;
+      const bool here = id[m] >= lo && id[m] < hi;
+      row[m] = here ? int(a.sd.pages ? entry_row(a.sd, b, id[m], nullptr) : base + id[m]) : -1;
+      w[m] = here ? __ldcg(a.weights + int64_t(i) * a.k + tid + m * kAThreads) : 0.0f;
     }
   };
-  int id[kAPer], id1[kAPer], id2[kAPer];
+  int row[kAPer], row1[kAPer], id1[kAPer], id2[kAPer];
   float w[kAPer], w1[kAPer];
-  fetch_ids(q0, id);
+  fetch_ids(q0, id2);
   fetch_ids(q0 + 1, id1);
-  fetch_weights(q0, id, w);
+  fetch_rows(q0, id2, row, w);
   for (int i = q0; i <= q0 + most; ++i) {
     fetch_ids(i + 2, id2);
-    fetch_weights(i + 1, id1, w1);
+    fetch_rows(i + 1, id1, row1, w1);
 #pragma unroll
     for (int m = 0; m < kAPer; ++m) {
-      if (id[m] >= 0) {
-        const int64_t row = entry_row(a.sd, b, id[m], nullptr);
-        if (row >= 0) atomicAdd(a.acc + row, w[m]);
-      }
-      id[m] = id1[m];
+      if (row[m] >= 0) atomicAdd(a.acc + row[m], w[m]);
+      row[m] = row1[m];
       w[m] = w1[m];
       id1[m] = id2[m];
     }
@@ -418,7 +417,7 @@ void launch_weights(const WeightArgs& a, cudaStream_t st) {
   else launch_tiles<2>(a, 4 * sms, st);
   if (!a.q_off) return;
   // parts of a sequence: the ids are read by each of them
-  const int P = int(std::max<int64_t>(1, std::min<int64_t>(16, 4 * int64_t(num_sms()) / a.B)));
+  const int P = int(std::max<int64_t>(1, std::min<int64_t>(16, 2 * int64_t(num_sms()) / a.B)));
   launch_k(k_accumulate, dim3(a.B, P), dim3(kAThreads), 0, st, a);
 }
 

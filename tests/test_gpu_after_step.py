@@ -94,6 +94,17 @@ def test_verify_rows_of_any_alignment_and_stride(pt, qt, lead):
     _check_verify(wide[:, lead:lead + V], wq[:, 6 - lead:6 - lead + V], tokens, off, u, r, M=6)
 
 
+@pytest.mark.parametrize("V,qt", [(262144, "bf16"), (300001, "f32"), (1000003, None)])
+def test_verify_large_vocabularies(V, qt):
+    """More partial sums than the scan keeps in registers."""
+    p, q, tokens, off, u, r = _problem(2, 3, V, 6)
+    _check_verify(p, None if qt is None else q.to(DT[qt]), tokens, off, u, r, M=4)
+    last = torch.zeros((1, V), device="cuda")
+    last[0, V - 1] = 0.5
+    got = _verify(last, None, [0], [0, 1], u, torch.tensor([1.0], device="cuda"))
+    assert list(host(got["t"])) == [V - 1]
+
+
 def test_verify_borders_are_exact():
     """Dyadic probabilities: every sum is exact, and a draw on a border takes the entry behind it."""
     V = 2500
@@ -309,6 +320,15 @@ def test_weights_of_candidates(lens, counts, k, page):
     assert torch.equal(again["acc"], got["acc"]) and torch.equal(again["w"], got["w"])
     bare = c.call(n_acc=n, want_weights=False)              # without the weights output
     assert torch.equal(bare["acc"], got["acc"])
+
+
+@pytest.mark.parametrize("page,scale_lo,scale_hi,qscale", [(0, 125, 128, 0.5), (512, 125, 128, 0.5), (0, 221, 227, 1e-28)])
+def test_weights_of_many_rows(page, scale_lo, scale_hi, qscale):
+    """Enough rows that a warp takes two tiles at a time; the last case has scales of 2^97 in some rows."""
+    c = WeightCase([3000, 700, 2000], [40, 0, 52], 1021, page, seed=11, scale_lo=scale_lo, scale_hi=scale_hi, qscale=qscale)
+    assert 92 * 64 > 32 * 148
+    c.check()
+    c.check(n_acc=[38, 0, 50])
 
 
 def test_weights_duplicates_and_positions_out_of_range():
