@@ -121,6 +121,8 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_Tensor = torch.Tensor
+
 # Element types of the C ABI's pointer arguments and the torch dtypes that
 # may carry them (same width, same kind of number).
 _KINDS = {
@@ -139,13 +141,13 @@ def _arg(fn, name, t, kind, numel=0):
     `numel` of them (the library cannot see buffer sizes)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise Csa2Error(-1, fn, f"{name}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype not in _KINDS[kind]:
         raise Csa2Error(-1, fn, f"{name}: {kind} elements expected, got {t.dtype}")
     if t.numel() < numel:
         raise Csa2Error(-1, fn, f"{name}: at least {numel} elements expected, got {t.numel()}")
-    return _ptr(t)
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
 
 
 def _queries(fn, n, q_codes, q_scales, w):
@@ -488,27 +490,24 @@ def csa2_sparse_attn_decode_noalloc(q, main_kv, seq_row_off, seq_len, topk, win,
 # after a step: verification of drafts, attention weights, eviction
 # ----------------------------------------------------------------------------
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def _launch(fn, tensors, stream, *args):
     """Calls `fn` on the device of its tensors (which must be one device, not
     necessarily the current one); stream None is that device's current stream."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()  # (-1: a host tensor)
-            if dev is None:
-                dev = d
-            elif d != dev:
-                raise Csa2Error(-1, fn, f"tensors on devices {dev} and {d}")
-    f = getattr(lib(), fn)
-    if dev is None or dev < 0:
+    devices = {t.get_device() for t in tensors if t is not None}  # (-1: a host tensor)
+    if len(devices) != 1:
+        raise Csa2Error(-1, fn, f"tensors on devices {sorted(devices)}")
+    dev = devices.pop()
+    f = getattr(_lib or lib(), fn)
+    if dev < 0:
         rc = f(*args, _stream(stream))
     else:
         # (the raw handle: torch.cuda.current_stream() builds a Stream object, 3.7 us)
-        st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-        if dev != torch.cuda.current_device():
+        st = stream.cuda_stream if stream is not None else _raw_stream(dev)
+        if dev != _current_device():
             with torch.cuda.device(dev):
                 rc = f(*args, st)
         else:
