@@ -536,9 +536,8 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
  *   seq_row_off [B] int64, seq_len [B] int32: the sequences' rows in main_kv
  *              (positions >= seq_len[b] are skipped, CSA2_DEV_INDEX_RANGE)
  *   q_off      [B+1] int32: sequence b owns queries q_off[b] .. q_off[b+1]-1
- *              (ascending within [0, Q]; others set CSA2_DEV_LENGTH and their
- *              sequence is not accumulated), or NULL: one query per sequence
- *              (Q == B)
+ *              (ascending within [0, Q]; else CSA2_DEV_LENGTH is set and no
+ *              query counts), or NULL: one query per sequence (Q == B)
  *   n_accept   [B] int32 or NULL (needs q_off): only the first n_accept[b] + 1
  *              queries of a sequence count, the ones that csa2_verify_drafts
  *              let stand (NULL: all; a negative number counts as 0)

@@ -869,10 +869,10 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
 
 // ---------------------------------------------------------------------------
 size_t csa2_attn_weights_workspace_bytes(int B, int Q, int k) {
-  (void)B;
-  if (Q < 0 || k < 0) return 0;
+  if (B < 0 || Q < 0 || k < 0) return 0;
   Carve c(nullptr);
   c.take<uint32_t>(kStatusBytes / 4);
+  c.take<int32_t>(size_t(B));
   c.take<float>(size_t(Q) * k);
   return c.used;
 }
@@ -901,9 +901,10 @@ csa2_status weights_impl(const char* fn, const uint16_t* q, const csa2_mxfp4_cac
     return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
   Carve c(workspace);
   uint32_t* status = c.take<uint32_t>(kStatusBytes / 4);
+  int32_t* counters = c.take<int32_t>(size_t(B));
   float* own = c.take<float>(size_t(Q) * k);
   launch_weights(WeightArgs{q, main_kv.codes, main_kv.scales, sd, q_off, n_accept, topk, k, lse, sm_scale, acc,
-                            weights_out ? weights_out : own, status, B, Q},
+                            weights_out ? weights_out : own, counters, status, B, Q},
                  static_cast<cudaStream_t>(stream));
   return check_launch(fn);
 }

@@ -296,6 +296,7 @@ struct WeightArgs {
   float sm_scale;
   float* acc;               // [cache rows]
   float* weights;           // [Q][k]
+  int32_t* counters;        // [B] arrival counters, zero between calls
   uint32_t* status;
   int B, Q;
 };

@@ -24,12 +24,12 @@
 // Order of the sums.  Entries are added in fp32 (weights of one query are at
 // most 16, sums grow over a sequence's life).  Where one query of a sequence
 // counts, k_weights adds itself.  Where several do, two of them may select
-// the same entry, and k_accumulate adds them in the order of the queries:
-// CTA p of a sequence owns the entries whose position falls into its part, a
-// barrier separates the queries (the next query's ids and weights are on
-// their way meanwhile).  A position listed twice in one selection
-// counts twice, as it does in the softmax; both additions have the same
-// value, so their order does not matter.
+// the same entry, and they are added in the order of the queries, a barrier
+// between two: by the last CTA of the sequence to finish, or (many queries) by
+// k_accumulate, whose CTA p of a sequence owns the entries whose position
+// falls into its part.  A position listed twice in one selection counts twice,
+// as it does in the softmax; both additions have the same value, so their
+// order does not matter.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -44,6 +44,7 @@ namespace {
 constexpr int kRow = kMainCodeBytes + kMainScaleBytes;  // 272 bytes: codes, then scales
 constexpr int kQStride = kD + 32;             // halves: rows g and g+1 lie 4 of 8 16-byte columns apart
 constexpr int kBlocks = kD / 32;              // 16 scale blocks
+constexpr int kLastK = 512;                   // longest selections that the last CTA of a sequence adds itself
 constexpr uint32_t kBig = 224;                // scale bytes from here on take the slow path (2^97 and more)
 
 // kTiles: MMA tiles (16 rows) of a warp's group.  Two tiles halve the shared
@@ -68,6 +69,7 @@ struct WSmem {
   float scale[C::kWarps][C::kRows][kBlocks];  // the current group's block scales
   float qexp[kHq];                            // power of two that undoes the query row's scaling
   float lse[kHq];
+  int last;
 };
 
 // Eight E2M1 codes (element 0 in the low nibble) -> four f16x2, exact.
@@ -113,28 +115,32 @@ __device__ __forceinline__ int64_t entry_row(const SegDesc& sd, int b, int64_t t
   return seg_row(sd, b, t, status);
 }
 
-// The sequence of query i, whether it counts, and whether others of its
-// sequence do.  q_off ascends, so the sequence is the number of sequences
-// that end at or before i.  Whole warp.
+// The sequence of query i, whether it counts, and the queries of its sequence
+// that do (the first one and how many follow it).  q_off ascends, so the
+// sequence is the number of sequences that end at or before i; offsets that do
+// not ascend within [0, Q] are reported and no query counts.  Whole warp.
 struct QueryRef {
-  int seq, counted, several;
+  int seq, counted, q0, more;
 };
 __device__ __forceinline__ QueryRef query_ref(const WeightArgs& a, int i, int lane) {
-  QueryRef r{i, 1, 0};
-  if (a.q_off == nullptr) return r;
-  int b = 0;
+  if (a.q_off == nullptr) return QueryRef{i, 1, i, 0};
+  int b = 0, prior = __ldg(a.q_off);
+  const int first = prior;
+  bool bad = first < 0;
   for (int j0 = 1; j0 <= a.B; j0 += 32) {
-    const int j = j0 + lane;
-    const bool before = j <= a.B && __ldg(a.q_off + j) <= i;
-    b += __popc(__ballot_sync(0xffffffffu, before));
+    const int j = j0 + lane, end = __ldg(a.q_off + min(j, a.B)), left = __shfl_up_sync(0xffffffffu, end, 1);
+    bad |= end < (lane ? left : prior) || end > a.Q;
+    prior = __shfl_sync(0xffffffffu, end, 31);
+    b += __popc(__ballot_sync(0xffffffffu, j <= a.B && end <= i));
   }
-  if (b >= a.B || __ldg(a.q_off) > i) return QueryRef{-1, 0, 0};
-  const int q0 = __ldg(a.q_off + b), q1 = __ldg(a.q_off + b + 1);
-  const int most = a.n_accept ? min(max(__ldg(a.n_accept + b), 0), q1 - q0 - 1) : q1 - q0 - 1;
-  r.seq = b;
-  r.counted = i - q0 <= most;
-  r.several = most > 0;
-  return r;
+  if (__any_sync(0xffffffffu, bad)) {
+    if (i == 0 && lane == 0) set_status(a.status, CSA2_DEV_LENGTH);
+    return QueryRef{-1, 0, 0, 0};
+  }
+  if (b >= a.B || first > i) return QueryRef{-1, 0, 0, 0};
+  const int q0 = __ldg(a.q_off + b), n = __ldg(a.q_off + b + 1) - q0;
+  const int more = a.n_accept ? min(max(__ldg(a.n_accept + b), 0), n - 1) : n - 1;
+  return QueryRef{b, i - q0 <= more, q0, more};
 }
 
 // Products of the warp's rows with the 16 heads: acc[m][h][0..1] row 16m + g,
@@ -178,6 +184,48 @@ __device__ __forceinline__ void products(const __half (&qs)[kHq][kQStride], cons
         }
       }
     }
+  }
+}
+
+// Adds the weights of queries q0 .. q0 + more of sequence b, in their order, to
+// the accumulators of positions lo .. hi-1.  Every thread of the CTA; at most
+// kPer * kThreads slots.  A thread's ids are fetched two queries ahead, the
+// cache rows and weights of those that lie in this part one ahead.
+template <int kPer, int kThreads>
+__device__ __forceinline__ void ordered_sums(const WeightArgs& a, int b, int q0, int more, int lo, int hi) {
+  const int tid = threadIdx.x;
+  auto fetch_ids = [&](int i, int (&id)[kPer]) {
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+      const int j = tid + m * kThreads;
+      id[m] = i <= q0 + more && j < a.k ? __ldg(a.topk + int64_t(i) * a.k + j) : -1;
+    }
+  };
+  const int64_t base = a.sd.pages ? 0 : a.sd.row_off[b];
+  auto fetch_rows = [&](int i, const int (&id)[kPer], int (&row)[kPer], float (&w)[kPer]) {
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+      const bool here = id[m] >= lo && id[m] < hi;
+      row[m] = here ? int(a.sd.pages ? entry_row(a.sd, b, id[m], nullptr) : base + id[m]) : -1;
+      w[m] = here ? __ldcg(a.weights + int64_t(i) * a.k + tid + m * kThreads) : 0.0f;
+    }
+  };
+  int row[kPer], row1[kPer], id1[kPer], id2[kPer];
+  float w[kPer], w1[kPer];
+  fetch_ids(q0, id2);
+  fetch_ids(q0 + 1, id1);
+  fetch_rows(q0, id2, row, w);
+  for (int i = q0; i <= q0 + more; ++i) {
+    fetch_ids(i + 2, id2);
+    fetch_rows(i + 1, id1, row1, w1);
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+      if (row[m] >= 0) atomicAdd(a.acc + row[m], w[m]);
+      row[m] = row1[m];
+      w[m] = w1[m];
+      id1[m] = id2[m];
+    }
+    __syncthreads();
   }
 }
 
@@ -337,64 +385,40 @@ __global__ void __launch_bounds__(Cfg<kTiles>::kThreads, Cfg<kTiles>::kBlocksPer
       if (at < 0 || v < 1.17549435e-38f) v = 0.0f;
       const int slot = grp * kWRows + r;
       if (slot < a.k) wout[slot] = v;
-      if (at >= 0 && !ref.several) atomicAdd(a.acc + at, v);
+      if (at >= 0 && ref.more == 0) atomicAdd(a.acc + at, v);
     }
+  }
+  if (kTiles == 1 && a.counters != nullptr && ref.more > 0) {
+    // Few queries: the last CTA of the sequence adds its weights.  The barrier
+    // orders every thread's stores before thread 0's release-acquire arrival.
+    __syncthreads();
+    if (tid == 0) {
+      int old;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counters + ref.seq) : "memory");
+      sm.last = old == (ref.more + 1) * int(gridDim.y) - 1;
+    }
+    __syncthreads();
+    if (!sm.last) return;
+    if (tid == 0) a.counters[ref.seq] = 0;
+    ordered_sums<kLastK / Cfg<kTiles>::kThreads, Cfg<kTiles>::kThreads>(a, ref.seq, ref.q0, ref.more, 0, int(len));
   }
 }
 
-// Sequences of which several queries count: their weights are added query by
-// query.  CTA (p, b) owns positions [len p / P, len (p+1) / P) of sequence b.
+// The same as a kernel of its own, for many queries: CTA (b, p) owns positions
+// [len p / P, len (p+1) / P) of sequence b.
 constexpr int kAThreads = 512;
-constexpr int kAPer = CSA2_MAX_TOPK / kAThreads;  // slots of a thread
 
 __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x;
   launch_dependents();
   grid_wait();
   const int q0 = __ldg(a.q_off + b), q1 = __ldg(a.q_off + b + 1);
-  const int most = a.n_accept ? min(max(__ldg(a.n_accept + b), 0), q1 - q0 - 1) : q1 - q0 - 1;
-  if (q0 < 0 || q1 < q0 || q1 > a.Q) {
-    if (blockIdx.y == 0 && tid == 0) set_status(a.status, CSA2_DEV_LENGTH);
-    return;
-  }
-  if (most <= 0) return;
+  if (q0 < 0 || q1 > a.Q) return;  // (k_weights has reported it, and every weight is 0)
+  const int more = a.n_accept ? min(max(__ldg(a.n_accept + b), 0), q1 - q0 - 1) : q1 - q0 - 1;
+  if (more <= 0) return;
   const int64_t len = seg_len_checked(a.sd, b, nullptr);
-  const int lo = int(len * blockIdx.y / gridDim.y), hi = int(len * (blockIdx.y + 1) / gridDim.y);
-  // This thread's slots of a query: its ids are fetched two queries ahead, the
-  // cache rows and weights of those that lie in this part one ahead.
-  auto fetch_ids = [&](int i, int (&id)[kAPer]) {
-#pragma unroll
-    for (int m = 0; m < kAPer; ++m) {
-      const int j = tid + m * kAThreads;
-      id[m] = i <= q0 + most && j < a.k ? __ldg(a.topk + int64_t(i) * a.k + j) : -1;
-    }
-  };
-  const int64_t base = a.sd.pages ? 0 : a.sd.row_off[b];
-  auto fetch_rows = [&](int i, const int (&id)[kAPer], int (&row)[kAPer], float (&w)[kAPer]) {
-#pragma unroll
-    for (int m = 0; m < kAPer; ++m) {
-      const bool here = id[m] >= lo && id[m] < hi;
-      row[m] = here ? int(a.sd.pages ? entry_row(a.sd, b, id[m], nullptr) : base + id[m]) : -1;
-      w[m] = here ? __ldcg(a.weights + int64_t(i) * a.k + tid + m * kAThreads) : 0.0f;
-    }
-  };
-  int row[kAPer], row1[kAPer], id1[kAPer], id2[kAPer];
-  float w[kAPer], w1[kAPer];
-  fetch_ids(q0, id2);
-  fetch_ids(q0 + 1, id1);
-  fetch_rows(q0, id2, row, w);
-  for (int i = q0; i <= q0 + most; ++i) {
-    fetch_ids(i + 2, id2);
-    fetch_rows(i + 1, id1, row1, w1);
-#pragma unroll
-    for (int m = 0; m < kAPer; ++m) {
-      if (row[m] >= 0) atomicAdd(a.acc + row[m], w[m]);
-      row[m] = row1[m];
-      w[m] = w1[m];
-      id1[m] = id2[m];
-    }
-    __syncthreads();
-  }
+  ordered_sums<CSA2_MAX_TOPK / kAThreads, kAThreads>(a, b, q0, more, int(len * blockIdx.y / gridDim.y),
+                                                     int(len * (blockIdx.y + 1) / gridDim.y));
 }
 
 template <int kTiles>
@@ -408,16 +432,27 @@ void launch_tiles(const WeightArgs& a, int64_t ctas, cudaStream_t st) {
 
 }  // namespace
 
-void launch_weights(const WeightArgs& a, cudaStream_t st) {
+void launch_weights(const WeightArgs& args, cudaStream_t st) {
+  WeightArgs a = args;
   // Two tiles per warp once there are more than 32 tiles per SM.  CTAs of a
   // query: as many as its slots allow while the grid stays at 16 (one tile)
   // or 4 (two) CTAs per SM, about a wave of those that run together.
   const int64_t tiles = int64_t(a.Q) * ((a.k + 15) / 16), sms = num_sms();
-  if (tiles <= 32 * sms) launch_tiles<1>(a, 16 * sms, st);
-  else launch_tiles<2>(a, 4 * sms, st);
+  if (tiles <= 32 * sms) {
+    // The last CTA of a sequence adds its weights where few slots make that
+    // short; else, and for many queries, a kernel of its own with several CTAs
+    // per sequence does (a second launch costs a caller about 2 us).
+    const bool last = a.k <= kLastK;
+    if (!last) a.counters = nullptr;
+    launch_tiles<1>(a, 16 * sms, st);
+    if (last) return;
+  } else {
+    a.counters = nullptr;
+    launch_tiles<2>(a, 4 * sms, st);
+  }
   if (!a.q_off) return;
   // parts of a sequence: the ids are read by each of them
-  const int P = int(std::max<int64_t>(1, std::min<int64_t>(16, 2 * int64_t(num_sms()) / a.B)));
+  const int P = int(std::max<int64_t>(1, std::min<int64_t>(16, 2 * sms / a.B)));
   launch_k(k_accumulate, dim3(a.B, P), dim3(kAThreads), 0, st, a);
 }
 

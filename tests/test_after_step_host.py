@@ -56,7 +56,7 @@ def _weights(q=FAKE, cache=None, off=FAKE, ln=FAKE, q_off=FAKE, n_acc=None, topk
     (dict(ws=None), -1), (dict(ws=FAKE + 16), -1), (dict(cache=C.MXFP4Cache(FAKE, FAKE, 1001)), -1),
     (dict(q_off=None), -1),                       # one query per sequence means Q == B
     (dict(q_off=None, Q=2, n_acc=FAKE), -1),      # accepted counts need q_off
-    (dict(wn=256 + 6 * 64 * 4 - 1), -3), (dict(Q=0), 0),
+    (dict(wn=256 + 256 + 6 * 64 * 4 - 1), -3), (dict(Q=0), 0),
 ])
 def test_weights_refuses(bad, rc):
     assert _weights(**bad) == rc

@@ -348,6 +348,22 @@ def test_weights_duplicates_and_positions_out_of_range():
     assert far["flags"] & 2 and not host(far["w"])[3:].any()
 
 
+@pytest.mark.parametrize("k", [64, 700])
+@pytest.mark.parametrize("off", [[0, 3, 2], [0, 4, 7], [-1, 2, 5], [0, 6, 5]])
+def test_weights_refuse_offsets_that_do_not_ascend(off, k):
+    c = WeightCase([500, 800], [3, 2], k, seed=5)
+    good = c.call()
+    keep, c.q_off = c.q_off, np.array(off, np.int32)
+    got = c.call()
+    assert got["flags"] == 8 and not host(got["w"]).any() and np.array_equal(host(got["acc"]), c.acc)
+    c.q_off = np.array([1, 3, 4], np.int32)                 # queries of no sequence weigh nothing
+    got = c.call()
+    w = host(got["w"])
+    assert got["flags"] == 0 and not w[0].any() and not w[4].any() and w[1:4].all(1).sum() >= 1
+    c.q_off = keep
+    assert torch.equal(c.call()["acc"], good["acc"])
+
+
 def test_weights_bad_page_is_skipped():
     c = WeightCase([1200, 600], [2, 1], 100, page=512, seed=6)
     good = host(c.call()["w"])
