@@ -50,6 +50,7 @@ struct __align__(16) SelSmem {
   uint32_t hist[kBins];       // this CTA's counts of the current digit
   uint32_t total[kBins];      // the cluster's
   uint32_t list[kList];       // this CTA's entries of the threshold's bin
+  uint8_t from[kList];        // and the warps that have them
   uint32_t all[kList];        // the cluster's
   uint32_t scan[kEWarps];
   uint32_t listed, gathered;
@@ -99,10 +100,6 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v, int lane) {
   return v;
 }
 
-// 31-bit rank of a weight among those of its sign: of a positive one its bits,
-// of a negative one or a NaN its rank key (NaN lowest).
-__device__ __forceinline__ uint32_t side_key(float f, bool neg) { return neg ? rank_key(f) : __float_as_uint(f); }
-
 __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int warp_cap) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
@@ -136,17 +133,28 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   const float* base = a.src.pages ? nullptr : a.acc_src + a.src.row_off[b];
   // (a step never crosses a page)
   auto step_at = [&](int q0) { return base ? base + q0 : a.acc_src + seg_row(a.src, b, q0, a.status); };
-  // The whole warp over its part from `from`, 4 consecutive positions per
-  // lane: fn(position, four weights), kBatch steps' loads in flight.
-  // Accumulators come in groups of 8, so the four lie inside them; positions
-  // behind the end of the sequence and protected ones are for fn to leave out.
+  // The whole warp over its part, 4 consecutive positions per lane and step:
+  // fn(position, four weights), from the accumulators on (kBatch steps' loads
+  // in flight) or from shared memory as far as it goes.  Entries that do not
+  // compete (protected ones, positions behind the end) come as NaN.
+  // Accumulators come in groups of 8, so a lane's four lie inside them.
+  auto mask = [&](int q0, float4 f) {
+    if (q0 < m0 || q0 + kStep > m1) {
+      const int q = q0 + 4 * lane;
+      const float no = __uint_as_float(0x7FC00000u);
+      if (q < m0 || q >= m1) f.x = no;
+      if (q + 1 < m0 || q + 1 >= m1) f.y = no;
+      if (q + 2 < m0 || q + 2 >= m1) f.z = no;
+      if (q + 3 < m0 || q + 3 >= m1) f.w = no;
+    }
+    return f;
+  };
   auto from_global = [&](int from, auto&& fn) {
     for (int q0 = from; q0 < w1; q0 += kBatch * kStep) {
       float4 f[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kStep + 4 * lane;
-        if (q < w1) {
+        if (q0 + i * kStep + 4 * lane < w1) {
           const float* src = step_at(q0 + i * kStep) + 4 * lane;
           f[i] = vec ? __ldg(reinterpret_cast<const float4*>(src))
                      : make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
@@ -154,28 +162,18 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (q0 + i * kStep + 4 * lane < w1) fn(q0 + i * kStep + 4 * lane, f[i]);
+        if (q0 + i * kStep < w1) fn(q0 + i * kStep, f[i]);
     }
   };
   auto each = [&](auto&& fn) {
 #pragma unroll 2
-    for (int q = w0 + 4 * lane; q < wc; q += kStep) fn(q, *reinterpret_cast<const float4*>(mine + (q - w0)));
-    from_global(w0 + warp_cap, fn);
+    for (int q0 = w0; q0 < wc; q0 += kStep)
+      fn(mask(q0, *reinterpret_cast<const float4*>(mine + (q0 - w0) + 4 * lane)));
+    from_global(w0 + warp_cap, [&](int q0, float4 f) { fn(mask(q0, f)); });
   };
-  // fn(weight) for those of the four that compete.
-  auto competing = [&](int q, float4 f, auto&& fn) {
-    if (q >= m0 && q + 4 <= m1) {
-      fn(f.x), fn(f.y), fn(f.z), fn(f.w);
-    } else {
-      if (q >= m0 && q < m1) fn(f.x);
-      if (q + 1 >= m0 && q + 1 < m1) fn(f.y);
-      if (q + 2 >= m0 && q + 2 < m1) fn(f.z);
-      if (q + 3 >= m0 && q + 3 < m1) fn(f.w);
-    }
-  };
-  // Sums every warp's (gt, eq) over the CTA and hands the sums to the cluster;
-  // slot 0: above and at 0, slot 1: above and at the threshold.
-  auto share = [&](int slot, uint32_t gt, uint32_t eq) {
+  // Every warp's counts (sm.warp_gt / warp_eq) summed over the CTA and handed
+  // to the cluster; slot 0: above and at 0, slot 1: above and at the threshold.
+  auto put = [&](uint32_t gt, uint32_t eq) {
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
@@ -183,6 +181,8 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       sm.warp_eq[warp] = eq;
     }
     __syncthreads();
+  };
+  auto share = [&](int slot) {
     if (warp == 0) {
       const uint32_t g = __reduce_add_sync(0xffffffffu, sm.warp_gt[lane]);
       const uint32_t e = __reduce_add_sync(0xffffffffu, sm.warp_eq[lane]);
@@ -195,14 +195,14 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   };
   uint32_t gt = 0, eq = 0;
   // ---- the weights, and how many lie above 0 and at 0 ----
-  from_global(w0, [&](int q, float4 f) {
-    if (q < wc) *reinterpret_cast<float4*>(mine + (q - w0)) = f;
-    competing(q, f, [&](float x) {
-      gt += x > 0.0f;
-      eq += x == 0.0f;
-    });
+  from_global(w0, [&](int q0, float4 f) {
+    if (q0 < wc) *reinterpret_cast<float4*>(mine + (q0 - w0) + 4 * lane) = f;
+    f = mask(q0, f);
+    gt += uint32_t(f.x > 0.0f) + uint32_t(f.y > 0.0f) + uint32_t(f.z > 0.0f) + uint32_t(f.w > 0.0f);
+    eq += uint32_t(f.x == 0.0f) + uint32_t(f.y == 0.0f) + uint32_t(f.z == 0.0f) + uint32_t(f.w == 0.0f);
   });
-  share(0, gt, eq);
+  put(gt, eq);
+  share(0);
   int slot = 0;
   uint32_t left = uint32_t(p.need);
   float thr = 0.0f;  // the threshold (NaN: NaN entries are the least that stay)
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
     slot = 1;
     const bool neg = left > above0;
     if (neg) left -= above0 + at0;
-    uint32_t known = 0, mask = 0;  // the threshold's rank, and which bits of it are known
+    uint32_t known = 0, mask_bits = 0;  // the threshold's rank, and which bits of it are known
     // The bin of `counts` that holds the left-th largest, among bins that
     // thread t owns (2047 - 2t and 2046 - 2t); zeroes the histogram.
     auto find = [&](const uint32_t* counts, int shift, uint32_t width) {
@@ -235,23 +235,40 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       __syncthreads();
       left -= sm.above;
       known |= sm.bin << shift;
-      mask |= width << shift;
+      mask_bits |= width << shift;
     };
-    constexpr int kShift[3] = {20, 10, 0};
+    // fn(rank) for the entries of the threshold's sign.  Among the negative
+    // ones, NaN entries rank lowest, and those that do not compete have to be
+    // told from them.
+    auto ranks = [&](auto&& fn) {
+      if (!neg) {
+        each([&](float4 f) {
+          if (f.x > 0.0f) fn(__float_as_uint(f.x));
+          if (f.y > 0.0f) fn(__float_as_uint(f.y));
+          if (f.z > 0.0f) fn(__float_as_uint(f.z));
+          if (f.w > 0.0f) fn(__float_as_uint(f.w));
+        });
+      } else {
+        for (int q = w0 + lane; q < w1; q += 32) {
+          const float y = q < wc ? mine[q - w0] : __ldg(step_at(q / kStep * kStep) + q % kStep);
+          if (q >= m0 && q < m1 && !(y >= 0.0f)) fn(rank_key(y));
+        }
+      }
+    };
+    auto shift_of = [](int digit) { return digit == 0 ? 20 : digit == 1 ? 10 : 0; };
     int digit = 0;
     bool alone = false;
-    uint32_t x = 0, n = 0;  // alone: this thread's entry of the bin, and how many there are
+    uint32_t n = 0;  // alone: entries of the bin
     for (; digit < 3 && !alone; ++digit) {
-      const int shift = kShift[digit];
+      const int shift = shift_of(digit);
       const uint32_t width = digit == 0 ? 2047u : 1023u;
-      each([&](int q, float4 f) {
-        competing(q, f, [&](float y) {
-          if (neg ? !(y >= 0.0f) : y > 0.0f) {
-            const uint32_t k = side_key(y, neg);
-            if ((k & mask) == known) atomicAdd(&sm.hist[(k >> shift) & width], 1u);
-          }
+      if (digit == 0) {
+        ranks([&](uint32_t k) { atomicAdd(&sm.hist[k >> 20], 1u); });
+      } else {
+        ranks([&](uint32_t k) {
+          if ((k & mask_bits) == known) atomicAdd(&sm.hist[(k >> shift) & width], 1u);
         });
-      });
+      }
       // CTA r adds its share of the bins over the cluster and hands the sums to all
       cl.sync();
       const int per = (kBins + C - 1) / C;
@@ -268,14 +285,18 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       alone = digit < 2 && n <= uint32_t(kList);
     }
     if (alone) {
-      each([&](int q, float4 f) {
-        competing(q, f, [&](float y) {
-          if (neg ? !(y >= 0.0f) : y > 0.0f) {
-            const uint32_t k = side_key(y, neg);
-            if ((k & mask) == known) sm.list[atomicAdd(&sm.listed, 1u)] = k;
-          }
-        });
+      // list the bin's entries, count those above the bin on the way
+      gt = 0;
+      ranks([&](uint32_t k) {
+        const uint32_t high = k & mask_bits;
+        gt += high > known;
+        if (high == known) {
+          const uint32_t at = atomicAdd(&sm.listed, 1u);
+          sm.list[at] = k;
+          sm.from[at] = uint8_t(warp);
+        }
       });
+      put(gt, 0);
       cl.sync();
       const int group = kEThreads / C, src = tid / group;
       if (src < C) {
@@ -284,33 +305,38 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
         for (uint32_t i = tid % group; i < m; i += group) sm.all[atomicAdd(&sm.gathered, 1u)] = from[i];
       }
       __syncthreads();
-      x = uint32_t(tid) < n ? sm.all[tid] : 0u;
+      const uint32_t x = uint32_t(tid) < n ? sm.all[tid] : 0u;
       for (; digit < 3; ++digit) {
-        const int shift = kShift[digit];
-        if (uint32_t(tid) < n && (x & mask) == known) atomicAdd(&sm.hist[(x >> shift) & 1023u], 1u);
+        const int shift = shift_of(digit);
+        if (uint32_t(tid) < n && (x & mask_bits) == known) atomicAdd(&sm.hist[(x >> shift) & 1023u], 1u);
         __syncthreads();
         find(sm.hist, shift, 1023u);
       }
-    }
-    thr = neg ? (known == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(~known)) : __uint_as_float(known);
-    // ---- entries above and at the threshold ----
-    gt = eq = 0;
-    if (thr == thr) {
-      each([&](int q, float4 f) {
-        competing(q, f, [&](float y) {
-          gt += y > thr;
-          eq += y == thr;
-        });
-      });
+      // this CTA's listed entries above and at the threshold
+      if (uint32_t(tid) < sm.listed) {
+        const uint32_t k = sm.list[tid];
+        if (k >= known) atomicAdd(k > known ? &sm.warp_gt[sm.from[tid]] : &sm.warp_eq[sm.from[tid]], 1u);
+      }
     } else {
-      each([&](int q, float4 f) {
-        competing(q, f, [&](float y) {
-          gt += y == y;
-          eq += y != y;
-        });
+      gt = eq = 0;
+      ranks([&](uint32_t k) {
+        gt += k > known;
+        eq += k == known;
       });
+      put(gt, eq);
     }
-    share(1, gt, eq);
+    if (neg) {
+      // the entries at or above 0 are above the threshold too
+      uint32_t up = 0;
+      each([&](float4 f) {
+        up += uint32_t(f.x >= 0.0f) + uint32_t(f.y >= 0.0f) + uint32_t(f.z >= 0.0f) + uint32_t(f.w >= 0.0f);
+      });
+      up = __reduce_add_sync(0xffffffffu, up);
+      if (lane == 0) atomicAdd(&sm.warp_gt[warp], up);
+    }
+    __syncthreads();
+    thr = neg ? (known == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(~known)) : __uint_as_float(known);
+    share(1);
   }
   // (that barrier followed the last access to another CTA's memory, and every
   // CTA's read of the length: seq_len_out may be seq_len itself)
@@ -462,8 +488,8 @@ csa2_status launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int64_t fit = (int64_t(226) * 1024 - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
   const int warp_cap = int(std::min(part, fit)) * kStep;
   const size_t smem = sizeof(SelSmem) + size_t(warp_cap) * 4 * kEWarps;
-  cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (smem > 48 * 1024) cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (C > 8) cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   launch_k_cluster(k_evict_select, dim3(C, a.B), dim3(kEThreads), smem, st, C, a, warp_cap);
   const csa2_status rc = check_launch("csa2_cache_evict");
   if (rc != CSA2_OK) return rc;

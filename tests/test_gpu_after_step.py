@@ -538,6 +538,15 @@ def test_evict_long_sequences(lens, keep, kind):
     c.check([keep] * len(lens), keep, first=4, last=128)
 
 
+@pytest.mark.parametrize("kind,share", [("ties", 0.2), ("ties", 0.5), ("ties", 0.9), ("odd", 0.3), ("odd", 0.6), ("odd", 0.85),
+                                        ("odd", 0.97)])
+@pytest.mark.parametrize("lens", [[70001, 9000], [900001]])
+def test_evict_long_sequences_at_every_threshold(kind, share, lens):
+    """Thresholds among many equal weights, among negative ones, and among NaN, over several CTAs."""
+    c = EvictCase(lens, kind, idx=False, seed=3)
+    c.check([int(n * share) for n in lens], max(lens), first=3, last=130)
+
+
 @pytest.mark.parametrize("B", [1, 3, 10, 20, 40, 80, 200])
 def test_evict_batches(B):
     c = EvictCase([(977 * (b + 1)) % 9001 for b in range(B)], "mixed", idx=B % 2 == 0, seed=B)
