@@ -497,7 +497,8 @@ csa2_status csa2_sparse_attn_decode_noalloc(const uint16_t* q, csa2_mxfp4_cache 
  *   draft      the same with its own type and stride, or NULL
  *   tokens     [Q] int32 token of every candidate;  q_off [B+1] int32
  *   u          [Q] fp32 random numbers of the tests in [0, 1) (u_i of row i)
- *   r          [B] fp32 random numbers of the draws in [0, 1)
+ *   r          [B] fp32 random numbers of the draws in [0, 1) (from 1 on: the
+ *              last token with a weight; below 0 or NaN: as 0)
  *   seq_len_in, seq_len_out  [B] int32 or both NULL: the cache lengths with
  *              all n candidates appended, and without the rejected ones
  *              (seq_len_in - (n - 1 - n_accept)); may be the same array.
@@ -597,7 +598,8 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
  * `dst_pages` may be one that `pages` names for an entry of any sequence.  A
  * sequence that does not fit its destination is left out (n = 0,
  * CSA2_DEV_ROW_LAYOUT); rows whose destination page id lies outside the cache
- * are not written (the same flag).
+ * are not written, and a source page id outside it reads page 0 (the same
+ * flag).  B <= 65535, max_len and max_keep <= 2^30.
  * ------------------------------------------------------------------------- */
 size_t csa2_cache_evict_workspace_bytes(int B, int max_len);
 csa2_status csa2_cache_evict(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,

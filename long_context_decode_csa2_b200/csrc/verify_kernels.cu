@@ -17,10 +17,10 @@
 //
 // Work split.  Only the stop row of a sequence is read (n - 1 tests read
 // single elements), by S CTAs, all sequences' at once: a warp takes a segment
-// of 256 elements at a time and leaves its fp64 sum in the workspace; the last CTA of the sequence to finish
-// scans them, and one of its warps reads the segment that holds r C_V again
-// (from L2) to find the token.  The sums do not depend on S or on the order
-// of arrival.  Bound by the chain of dependent steps (tests 2 us, arrival
+// of 256 elements at a time and leaves its fp64 sum in the workspace; the last
+// CTA of the sequence to finish scans them, and one of its warps reads the
+// segment that holds r C_V again (from L2) to find the token.  The sums do not
+// depend on S or on the order of arrival.  Bound by the chain of dependent steps (tests 2 us, arrival
 // 1 us, scan and second read 3 us) until the rows are tens of MB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(VerifyArgs a) {
     if (!sm.last) return;
   }
   // ---- the last CTA draws the token ----
-  const float r = a.r[b];
+  const float r = fmaxf(a.r[b], 0.0f);  // (NaN draws as 0)
   find_segment(part, nseg, r, sm);
   if (!(sm.total > 0.0) && rejected) {
     // p <= q everywhere: the residual is empty, the token comes from p (one

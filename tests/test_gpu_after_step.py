@@ -114,6 +114,9 @@ def test_verify_borders_are_exact():
     got = _verify(p, None, [0] * 8, list(range(9)), torch.zeros(8, device="cuda"), r)
     assert list(host(got["t"])) == [3, 1000, 1024, 2499, 2499, 3, 2499, 1024] and got["flags"] == 0
     _check_verify(p, None, [0] * 8, list(range(9)), torch.zeros(8, device="cuda"), r)
+    odd = torch.tensor([float("nan"), -1.0, 1.5, float("inf")], device="cuda")
+    got = _verify(p[:4], None, [0] * 4, list(range(5)), torch.zeros(4, device="cuda"), odd)
+    assert list(host(got["t"])) == [3, 3, 2499, 2499]      # r outside [0, 1)
     # tests at the border: u q < p is strict
     p2 = torch.tensor([[0.25, 0.75], [0.5, 0.5]], device="cuda").repeat(4, 1)
     q2 = torch.tensor([[0.5, 0.5], [0.5, 0.5]], device="cuda").repeat(4, 1)
@@ -551,6 +554,11 @@ def test_evict_long_sequences_at_every_threshold(kind, share, lens):
 def test_evict_batches(B):
     c = EvictCase([(977 * (b + 1)) % 9001 for b in range(B)], "mixed", idx=B % 2 == 0, seed=B)
     c.check([(311 * (b + 2)) % 5000 for b in range(B)], 5000, first=1, last=8, max_len=20000)
+
+
+def test_evict_nothing():
+    EvictCase([0, 0], seed=1).check([3, 0], 4, first=1, last=1, max_len=0)
+    EvictCase([0, 5], page=512, seed=1).check([0, 0], 1)
 
 
 def test_evict_flags():
