@@ -38,7 +38,6 @@ constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVec = 8;                       // consecutive elements per lane and step
 constexpr int kSeg = kVerifySegment;          // elements of one partial sum: 8 per lane
-constexpr int kFly = 1;                       // segments of a warp whose loads are in flight together (32 warps per SM)
 static_assert(kSeg == 32 * kVec, "a segment is one vector per lane");
 
 struct NoDraft {};  // drafts without probabilities
@@ -134,12 +133,11 @@ __device__ __forceinline__ double weight_of(float x, float y, const StopRow<TQ>&
   }
 }
 
-// w[i]: this lane's 8 weights of segment seg + i, the loads of all kN segments
-// in flight together.  Segments at an edge, whose covering words would leave
-// the row (or that lie behind it), are read element by element.
-template <int kN, class TP, class TQ>
-__device__ __forceinline__ void segment_weights(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, int lane,
-                                                double (&w)[kN][kVec]) {
+// fn(i, weights): this lane's 8 weights of segment seg + i, the loads of all kN
+// segments in flight together.  Segments at an edge, whose covering words would
+// leave the row (or that lie behind it), are read element by element.
+template <int kN, class TP, class TQ, class F>
+__device__ __forceinline__ void each_segment(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, int lane, F&& fn) {
   constexpr bool kDraft = !std::is_same<TQ, NoDraft>::value;
   using QT = typename std::conditional<kDraft, TQ, float>::type;
   const int64_t e0 = int64_t(seg) * kSeg;
@@ -160,24 +158,24 @@ __device__ __forceinline__ void segment_weights(const TP* p, const StopRow<TQ>& 
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       float x[kVec], y[kVec] = {};
+      double w[kVec];
       pr[i].unpack(pm, x);
       if (kDraft && q != nullptr) qr[i].unpack(qm, y);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) w[i][j] = weight_of(x[j], y[j], s, e0 + i * kSeg + lane * kVec + j);
+      for (int j = 0; j < kVec; ++j) w[j] = weight_of(x[j], y[j], s, e0 + i * kSeg + lane * kVec + j);
+      fn(i, w);
     }
   } else {
 #pragma unroll 1
     for (int i = 0; i < kN; ++i) {
       float x[kVec], y[kVec] = {};
+      double w[kVec];
       const int64_t e = e0 + i * kSeg + lane * kVec;
       load8_edge(p, e, V, x);
       if (kDraft && q != nullptr) load8_edge(q, e, V, y);
 #pragma unroll
-      for (int m = 0; m < kN; ++m)
-        if (m == i) {
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) w[m][j] = weight_of(x[j], y[j], s, e + j);
-        }
+      for (int j = 0; j < kVec; ++j) w[j] = weight_of(x[j], y[j], s, e + j);
+      fn(i, w);
     }
   }
 }
@@ -196,20 +194,28 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {  // inclusive
   return v;
 }
 
-// Sums of segments seg .. seg + kFly - 1 (those below nseg) to part.
+// Segments of a warp whose loads are in flight together, with 32 warps per SM
+// (64 x 131072 fp32 p and q: 19.3 us with one, 18.0 with two, spills with more;
+// 256 x 50001 fp16 p: 17.6, 17.2 and 16.5 us with one, two and three).
+template <class TP, class TQ>
+constexpr int fly() {
+  constexpr int bytes = int(sizeof(TP)) + (std::is_same<TQ, NoDraft>::value ? 0 : int(sizeof(TQ)));
+  return bytes >= 4 ? 2 : 3;
+}
+
+// Sums of segments seg .. seg + fly - 1 (those below nseg) to part.
 template <class TP, class TQ>
 __device__ __forceinline__ void segment_sums(const TP* p, const StopRow<TQ>& s, int seg, int nseg, int64_t V, int lane,
                                              double* part) {
-  double w[kFly][kVec], mine = 0.0;
-  segment_weights<kFly>(p, s, seg, V, lane, w);
-#pragma unroll
-  for (int i = 0; i < kFly; ++i) {
+  constexpr int kFly = fly<TP, TQ>();
+  double mine = 0.0;
+  each_segment<kFly>(p, s, seg, V, lane, [&](int i, const double (&w)[kVec]) {
     double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) sum += w[i][j];
+    for (int j = 0; j < kVec; ++j) sum += w[j];
     sum = warp_sum(sum);
     if (lane == i) mine = sum;
-  }
+  });
   if (lane < kFly && seg + lane < nseg) __stcg(part + seg + lane, mine);
 }
 
@@ -218,18 +224,21 @@ __device__ __forceinline__ void segment_sums(const TP* p, const StopRow<TQ>& s, 
 template <class TP, class TQ>
 __device__ __forceinline__ int segment_find(const TP* p, const StopRow<TQ>& s, int seg, int64_t V, double base,
                                             double want, int lane) {
-  double w[1][kVec], sum = 0.0;
-  segment_weights<1>(p, s, seg, V, lane, w);
+  double w[kVec], sum = 0.0;
+  each_segment<1>(p, s, seg, V, lane, [&](int, const double (&v)[kVec]) {
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) sum += w[0][j];
+    for (int j = 0; j < kVec; ++j) w[j] = v[j];
+  });
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) sum += w[j];
   const double incl = warp_scan(sum, lane);
   double c = __shfl_up_sync(0xffffffffu, incl, 1);
   c = base + (lane == 0 ? 0.0 : c);
   int hit = -1, last = -1;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    c += w[0][j];
-    if (w[0][j] > 0.0) {
+    c += w[j];
+    if (w[j] > 0.0) {
       last = seg * kSeg + lane * kVec + j;
       if (hit < 0 && c > want) hit = last;
     }
@@ -393,6 +402,7 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(VerifyArgs a) {
   }
   const int nseg = (a.V + kSeg - 1) / kSeg;
   double* part = a.part + int64_t(b) * nseg;
+  constexpr int kFly = fly<TP, TQ>();
   for (int g = (blockIdx.y * kVWarps + warp) * kFly; g < nseg; g += gridDim.y * kVWarps * kFly)
     segment_sums(p, s, g, nseg, a.V, lane, part);
   __syncthreads();
@@ -456,7 +466,7 @@ void launch_verify(const VerifyArgs& a, cudaStream_t st) {
   // sequences run at once (four CTAs per SM): a second wave would repeat the
   // tests' chain of loads (64 rows of 131072: 23.5 us in three waves)
   const int nseg = (a.V + kSeg - 1) / kSeg;
-  const int S = std::max(1, std::min(4 * num_sms() / a.B, (nseg + kVWarps * kFly - 1) / (kVWarps * kFly)));
+  const int S = std::max(1, std::min(4 * num_sms() / a.B, (nseg + kVWarps - 1) / kVWarps));
   switch (a.target_type) {
     case CSA2_TYPE_F32: return launch_target<float>(a, S, st);
     case CSA2_TYPE_BF16: return launch_target<__nv_bfloat16>(a, S, st);
