@@ -531,8 +531,10 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
  * with key_j the dequantised main row as in csa2_sparse_attn_decode and lse
  * its output (window rows included, so a query's weights sum to at most 16).
  * Empty slots (-1), queries that do not count and heads with lse = -inf give
- * weight 0, and a weight below 2^-126 (the smallest normal fp32) is 0.  The queries of a sequence are added in their order (results do
- * not change from run to run); a position listed twice is added twice.
+ * weight 0, and a weight below 2^-126 (the smallest normal fp32) is 0.  The
+ * queries of a sequence are added in their order, so results do not change
+ * from run to run; a position listed twice is added twice.  (Sequences that
+ * share rows, by a page in both their tables, add to them in any order.)
  *   q          [Q][16][512] bf16;  topk [Q][k] int32;  lse [Q][16] fp32
  *   seq_row_off [B] int64, seq_len [B] int32: the sequences' rows in main_kv
  *              (positions >= seq_len[b] are skipped, CSA2_DEV_INDEX_RANGE)

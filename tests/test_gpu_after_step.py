@@ -473,7 +473,7 @@ class EvictCase:
         self.acc = a
         self.row_of, self.drow_of = _rows(self.off, self.table, page), _rows(self.doff, self.dtable, page)
 
-    def call(self, keep, max_keep, first=0, last=0, max_len=None, alias=False, ws=None, stream=None, dst=None):
+    def call(self, keep, max_keep, first=0, last=0, max_len=None, alias=False, ws=None, stream=None, dst=None, shift=0):
         B = len(self.lens)
         d = {"kept": torch.full((B, max_keep), -9, dtype=torch.int32, device="cuda"), "len": _i32(self.lens)}
         seq_len = d["len"] if alias else _i32(self.lens)
@@ -481,7 +481,7 @@ class EvictCase:
         dst = [p.clone() for p in self.dplanes] if dst is None else dst
         if self.page:
             src = dst                                        # one pool: source and destination pages of the same tensors
-        acc = dev(self.acc)
+        acc = dev(np.concatenate([np.zeros(shift, np.float32), self.acc]))[shift:]
         dacc = acc if self.page else torch.full((self.drows,), -5.0, device="cuda")
         cache = lambda p: (C.cache(p[0], p[1]), C.cache(p[2], p[3]) if self.idx else None)  # noqa: E731
         (ms, is_), (md, id_) = cache(src), cache(dst)
@@ -530,6 +530,7 @@ def test_evict_matches_the_plain_form(kind, page):
     c.check([-5] * 12, 1)
     c.check([10 ** 6] * 12, 9000)                           # everything stays
     c.check([3] * 12, 3, first=5, last=2)                   # fewer than are protected: the last ones, then the first
+    c.check(keep, 4500, first=1, last=7, shift=3)           # accumulators off the 16-byte grid
 
 
 @pytest.mark.parametrize("lens,keep", [([70001], 30000), ([300001, 5], 150000), ([1100000], 500001),
@@ -538,7 +539,7 @@ def test_evict_matches_the_plain_form(kind, page):
 def test_evict_long_sequences(lens, keep, kind):
     """Runs of positions longer than the shared memory that holds their keys, and every cluster size."""
     c = EvictCase(lens, kind, idx=False, seed=1)
-    c.check([keep] * len(lens), keep, first=4, last=128)
+    c.check([keep] * len(lens), keep, first=4, last=128, shift=len(lens) % 4)
 
 
 @pytest.mark.parametrize("kind,share", [("ties", 0.2), ("ties", 0.5), ("ties", 0.9), ("odd", 0.3), ("odd", 0.6), ("odd", 0.85),
