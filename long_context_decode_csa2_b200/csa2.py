@@ -490,7 +490,9 @@ def csa2_sparse_attn_decode_noalloc(q, main_kv, seq_row_off, seq_len, topk, win,
 # after a step: verification of drafts, attention weights, eviction
 # ----------------------------------------------------------------------------
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (absent from a torch built without CUDA, where no call gets that far)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -531,9 +533,11 @@ def _prob_rows(fn, name, t, Q, V):
     rows, cols = t.shape
     if rows < Q or cols != V:
         raise Csa2Error(-1, fn, f"{name}: [{Q}, {V}] expected, got [{rows}, {cols}]")
+    if t.is_contiguous():
+        return _arg(fn, name, t, "prob"), _PROB_TYPES[t.dtype], V
     if V > 1 and t.stride(1) != 1:
         raise Csa2Error(-1, fn, f"{name}: the probabilities of a row must be contiguous")
-    return _arg(fn, name, t if t.is_contiguous() else t[0], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
+    return _arg(fn, name, t[0], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
 
 
 def csa2_verify_drafts_workspace_bytes(B, V):

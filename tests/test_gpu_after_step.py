@@ -105,6 +105,16 @@ def test_verify_large_vocabularies(V, qt):
     assert list(host(got["t"])) == [V - 1]
 
 
+def test_verify_offsets_beyond_32_bits():
+    """Rows 1.2e9 elements apart: element offsets above 2^31, byte offsets above 2^32."""
+    V, far = 5003, 1_200_000_001
+    p, q, tokens, off, u, r = _problem(1, 3, V, 4)
+    big = torch.empty(2 * far + V, dtype=torch.bfloat16, device="cuda").as_strided((3, V), (far, 1))
+    big.copy_(p.to(torch.bfloat16))
+    _check_verify(big, q, tokens, off, u, r, M=3)
+    _check_verify(p, big, tokens, off, torch.zeros(3, device="cuda"), r, M=3)
+
+
 def test_verify_borders_are_exact():
     """Dyadic probabilities: every sum is exact, and a draw on a border takes the entry behind it."""
     V = 2500
