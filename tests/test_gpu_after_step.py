@@ -105,6 +105,17 @@ def test_verify_large_vocabularies(V, qt):
     assert list(host(got["t"])) == [V - 1]
 
 
+def test_verify_many_sequences_of_a_large_vocabulary():
+    """More partial sums per CTA than fit its shared memory: 700 sequences draw from one row of 300001 (stride 0)."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    V, B = 300001, 700
+    row = torch.rand(V, device="cuda", generator=g) ** 4
+    r = torch.rand(B, device="cuda", generator=g)
+    got = _verify(row.expand(B, V), None, [0] * B, list(range(B + 1)), torch.zeros(B, device="cuda"), r)
+    c = np.cumsum(_f64(row))
+    assert np.array_equal(host(got["t"]), np.searchsorted(c, _f64(r) * c[-1], side="right")) and got["flags"] == 0
+
+
 def test_verify_offsets_beyond_32_bits():
     """Rows 1.2e9 elements apart: element offsets above 2^31, byte offsets above 2^32."""
     V, far = 5003, 1_200_000_001
