@@ -91,12 +91,15 @@ __device__ __forceinline__ Plan make_plan(const EvictArgs& a, int b, uint32_t* s
   return p;
 }
 
-__device__ __forceinline__ uint32_t warp_incl(uint32_t v, int lane) {
+// Inclusive sum over the lanes up to this one (the shuffle's own predicate says
+// whether there is a lane d below).
+__device__ __forceinline__ uint32_t warp_incl(uint32_t v, int) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
+  for (int d = 1; d < 32; d <<= 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 o;\n\tshfl.sync.up.b32 o|p, %0, %1, 0, 0xffffffff;\n\t@p add.u32 %0, %0, o;\n\t}"
+        : "+r"(v)
+        : "r"(d));
   return v;
 }
 
@@ -274,9 +277,9 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       const int per = (kBins + C - 1) / C;
       for (int i = tid; i < per && rank * per + i < kBins; i += kEThreads) {
         uint32_t v = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < C; ++c) v += cl.map_shared_rank(sm.hist, c)[rank * per + i];
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < C; ++c) cl.map_shared_rank(sm.total, c)[rank * per + i] = v;
       }
       cl.sync();
@@ -383,14 +386,15 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
         }
       }
     }
-    const uint32_t flags = uint32_t(stays[0]) | uint32_t(stays[1]) << 8 | uint32_t(stays[2]) << 16 |
-                           uint32_t(stays[3]) << 24;
+    const uint32_t flags = (stays[0] ? 1u : 0u) + (stays[1] ? 1u << 8 : 0u) + (stays[2] ? 1u << 16 : 0u) +
+                           (stays[3] ? 1u << 24 : 0u);
     const uint32_t incl = warp_incl(flags, lane), sum = __shfl_sync(0xffffffffu, incl, 31);
     // four indexes from `at` (each below 128): entries of earlier groups of 32, and of lanes below
     const uint32_t idx = incl - flags + sum * 0x01010100u;
+    int32_t* to = kept + at;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (stays[i]) kept[at + ((idx >> (8 * i)) & 255u)] = q0 + 32 * i + lane;
+      if (stays[i]) to[__byte_perm(idx, 0, 0x4440 + i)] = q0 + 32 * i + lane;
     at += (sum * 0x01010101u) >> 24;
   };
   for (int q0 = w0; q0 < wc; q0 += kStep) {
