@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
 }
 
 constexpr int kMThreads = 256;
-// Destination rows of a CTA: 64 measured 270 us at four sequences of 2^20 cut
+// Destination rows of a CTA: 64 measured 264 us at four sequences of 2^20 cut
 // to half, 256 (fewer, longer CTAs with the same loads in flight) 296 us, and
 // a persistent grid that looks rows up one tile ahead 320 us.
 constexpr int kMRows = 64;
