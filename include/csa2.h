@@ -507,7 +507,8 @@ csa2_status csa2_sparse_attn_decode_noalloc(const uint16_t* q, csa2_mxfp4_cache 
  *   out_tokens [B][out_stride] int32 or NULL: the accepted tokens, then the
  *              next token, then -1 (a next token that does not fit sets
  *              CSA2_DEV_LENGTH)
- *   workspace  csa2_verify_drafts_workspace_bytes(B, V)
+ *   workspace  csa2_verify_drafts_workspace_bytes(B, V); one that is large
+ *              enough may serve calls of any B, Q and V in turn
  * ------------------------------------------------------------------------- */
 #define CSA2_TYPE_F32 0
 #define CSA2_TYPE_BF16 1
@@ -548,7 +549,8 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
  *              written.  The accumulator of a new entry starts at zero: keep
  *              it zero behind the sequences' ends
  *   weights_out [Q][k] fp32 or NULL
- *   workspace  csa2_attn_weights_workspace_bytes(B, Q, k)
+ *   workspace  csa2_attn_weights_workspace_bytes(B, Q, k); one that is
+ *              large enough may serve calls of any B, Q and k in turn
  * Accuracy: relative error of a weight <= 6e-6 * (1 + A), A the largest
  * sm_scale * sum_d |q_d key_d| of its heads (fp32 sums; bf16 queries and E2M1
  * codes enter exactly, but elements below 2^-39 of a query row's largest are

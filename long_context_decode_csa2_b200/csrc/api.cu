@@ -815,7 +815,7 @@ csa2_status csa2_sparse_attn_prefill(const uint16_t* q, const int32_t* q_pos, in
 namespace {
 struct VerifyWs {
   uint32_t* status;
-  int32_t* counters;  // [B], zero between calls
+  int32_t* counters;  // [kArrivalCounters], zero between calls
   double* part;       // [B][segments]
   size_t bytes;
 };
@@ -823,7 +823,7 @@ VerifyWs verify_ws(void* ws, int B, int V) {
   Carve c(ws);
   VerifyWs w;
   w.status = c.take<uint32_t>(kStatusBytes / 4);
-  w.counters = c.take<int32_t>(size_t(B));
+  w.counters = c.take<int32_t>(kArrivalCounters);
   w.part = c.take<double>(size_t(B) * ((size_t(V) + kVerifySegment - 1) / kVerifySegment));
   w.bytes = c.used;
   return w;
@@ -872,7 +872,7 @@ size_t csa2_attn_weights_workspace_bytes(int B, int Q, int k) {
   if (B < 0 || Q < 0 || k < 0) return 0;
   Carve c(nullptr);
   c.take<uint32_t>(kStatusBytes / 4);
-  c.take<int32_t>(size_t(B));
+  c.take<int32_t>(kArrivalCounters);
   c.take<float>(size_t(Q) * k);
   return c.used;
 }
@@ -901,7 +901,7 @@ csa2_status weights_impl(const char* fn, const uint16_t* q, const csa2_mxfp4_cac
     return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
   Carve c(workspace);
   uint32_t* status = c.take<uint32_t>(kStatusBytes / 4);
-  int32_t* counters = c.take<int32_t>(size_t(B));
+  int32_t* counters = c.take<int32_t>(kArrivalCounters);
   float* own = c.take<float>(size_t(Q) * k);
   launch_weights(WeightArgs{q, main_kv.codes, main_kv.scales, sd, q_off, n_accept, topk, k, lse, sm_scale, acc,
                             weights_out ? weights_out : own, counters, status, B, Q},

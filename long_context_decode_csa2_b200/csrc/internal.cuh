@@ -255,6 +255,11 @@ struct CompressArgs {
 };
 void launch_compress(const CompressArgs& a, cudaStream_t st);
 
+// Arrival counters of csa2_verify_drafts and csa2_attn_weights: a fixed number
+// at a fixed place behind the status block, so that a workspace that has served
+// one batch size holds no scratch where another one's counters lie.
+constexpr int kArrivalCounters = 1024;
+
 // Verification of drafted tokens: per sequence the accepted prefix of its
 // candidates and the next token.
 constexpr int kVerifySegment = 256;   // vocabulary entries of one partial sum
@@ -277,7 +282,7 @@ struct VerifyArgs {
   int32_t* out_tokens;     // [B][out_stride] or null
   int out_stride;
   double* part;            // workspace: [B][ceil(V / kVerifySegment)] sums
-  int32_t* counters;       // [B] arrival counters, zero between calls
+  int32_t* counters;       // [kArrivalCounters], zero between calls (larger batches: one CTA per sequence)
   uint32_t* status;
 };
 void launch_verify(const VerifyArgs& a, cudaStream_t st);
@@ -296,7 +301,7 @@ struct WeightArgs {
   float sm_scale;
   float* acc;               // [cache rows]
   float* weights;           // [Q][k]
-  int32_t* counters;        // [B] arrival counters, zero between calls
+  int32_t* counters;        // [kArrivalCounters], zero between calls (larger batches: k_accumulate)
   uint32_t* status;
   int B, Q;
 };

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(VerifyArgs a) {
       a.n_accept[b] = acc;
       a.next_tok[b] = tok;
       if (a.seq_len_out) a.seq_len_out[b] = a.seq_len_in[b] - (n - 1 - acc);
-      a.counters[b] = 0;
+      if (gridDim.y > 1) a.counters[b] = 0;
       if (out && acc < a.out_stride) out[acc] = tok;
       if (out && acc >= a.out_stride) set_status(a.status, CSA2_DEV_LENGTH);
     }
@@ -466,7 +466,9 @@ void launch_verify(const VerifyArgs& a, cudaStream_t st) {
   // sequences run at once (four CTAs per SM): a second wave would repeat the
   // tests' chain of loads (64 rows of 131072: 23.5 us in three waves)
   const int nseg = (a.V + kSeg - 1) / kSeg;
-  const int S = std::max(1, std::min(4 * num_sms() / a.B, (nseg + kVWarps - 1) / kVWarps));
+  const int S = a.B > kArrivalCounters
+                    ? 1
+                    : std::max(1, std::min(4 * num_sms() / a.B, (nseg + kVWarps - 1) / kVWarps));
   switch (a.target_type) {
     case CSA2_TYPE_F32: return launch_target<float>(a, S, st);
     case CSA2_TYPE_BF16: return launch_target<__nv_bfloat16>(a, S, st);

@@ -442,7 +442,7 @@ void launch_weights(const WeightArgs& args, cudaStream_t st) {
     // The last CTA of a sequence adds its weights where few slots make that
     // short; else, and for many queries, a kernel of its own with several CTAs
     // per sequence does (a second launch costs a caller about 2 us).
-    const bool last = a.k <= kLastK;
+    const bool last = a.k <= kLastK && a.B <= kArrivalCounters;
     if (!last) a.counters = nullptr;
     launch_tiles<1>(a, 16 * sms, st);
     if (last) return;

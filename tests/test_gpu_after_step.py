@@ -697,6 +697,33 @@ def test_calls_capture_and_replay():
     assert all(C.device_status(ws) == 0 for ws in wa + wb)
 
 
+def test_one_workspace_serves_batches_of_any_size():
+    """Large and small batches in turn on one workspace: neither's scratch lies where the other counts arrivals."""
+    few, many = WeightCase([900] * 3, [6] * 3, 512, seed=1), WeightCase([70] * 150, [2] * 150, 64, seed=2)
+    size = C.csa2_attn_weights_workspace_bytes
+    ws = C.workspace(max(size(3, 18, 512), size(150, 300, 64)))
+    cases = (few, many)
+    want = [c.call()["acc"] for c in cases]
+    for i in (0, 1, 0, 1):
+        got = cases[i].call(want_weights=False, ws=ws)
+        assert torch.equal(got["acc"], want[i]) and got["flags"] == 0
+    a, b = _problem(2, 4, 131072, 3), _problem(140, 3, 5003, 4)
+    size = C.csa2_verify_drafts_workspace_bytes
+    ws = C.workspace(max(size(2, 131072), size(140, 5003)))
+    for p, q, tokens, off, u, r in (a, b, a, b):
+        got = _verify(p, q, tokens, off, u, r, ws=ws)
+        n, t = R.verify(_f64(p), _f64(q), tokens, off, _f64(u), _f64(r))
+        assert np.array_equal(host(got["n"]), n) and np.array_equal(host(got["t"]), t) and got["flags"] == 0
+
+
+@pytest.mark.parametrize("B", [1023, 1024, 1025, 1100])
+def test_more_sequences_than_arrival_counters(B):
+    """Few queries over many sequences, most of them without any."""
+    counts = np.zeros(B, np.int64)
+    counts[[0, B // 2, B - 1]] = 3
+    WeightCase(np.full(B, 40), counts, 32, seed=B).check()
+
+
 def test_calls_on_two_streams_at_once():
     c1, c2 = WeightCase([900], [4], 128, seed=1), WeightCase([900], [4], 128, seed=2)
     e1, e2 = EvictCase([9000], seed=1), EvictCase([9000], seed=2)
