@@ -38,7 +38,6 @@ entries that carried the most of it.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 from dataclasses import dataclass
 
@@ -199,9 +198,12 @@ class DecodeStep:
         # ratio 2: one pending-token state per Full layer's caches
         n_full = sum(1 for m in pattern if m == "F")
         self.pairs = [PairStream(B, dev, projection) for _ in range(n_full)] if ratio == 2 else []
-        # after-step calls (verify, accumulate): made at their first use
-        self.ws_verify = self.ws_weights = None
-        self.n_accept = self.next_tok = None
+        # after-step calls (verify, accumulate): scratch made at their first use.
+        # A larger vocabulary adds to ws_verify: graphs captured before it go on
+        # using what they were captured with
+        self.ws_verify = []
+        self.ws_weights = None
+        self.n_accept, self.next_tok = (torch.empty(B, dtype=torch.int32, device=dev) for _ in range(2))
         # optional callable(call_name, "begin" | "end", stream), e.g. to record events
         self.hook = None
 
@@ -397,10 +399,18 @@ class DecodeStep:
             main.wait_event(self.ev_group[self.plan[-1][0]][g])
         return self.out
 
-    @staticmethod
-    def _filling(stream):
-        """Scratch made at its first use is zero-filled on the stream that uses it."""
-        return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+    def _scratch(self, nbytes, stream):
+        """Scratch made at a call's first use, zero-filled on the stream that
+        uses it.  Not while that stream is captured: only the graph's replays
+        would fill it."""
+        dev = self.out.device
+        if dev.type != "cuda":
+            return C.workspace(nbytes, dev)
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("the first verify (of a vocabulary this large) and the first accumulate of a step make "
+                                 "its scratch: call them once before their capture")
+            return C.workspace(nbytes, dev)
 
     def verify(self, target, tokens, q_off, u, r, draft=None, seq_len=None, out_tokens=None, stream=None):
         """After a verification step: which candidates stand, and the next
@@ -408,17 +418,14 @@ class DecodeStep:
         [Q, V] probabilities behind / for every candidate, tokens [Q], u [Q]
         and r [B] random numbers.  seq_len [B], if given, holds the lengths
         with all candidates appended and drops the rejected ones in place.
-        Returns (n_accept, next_tok), tensors that the next call overwrites."""
+        Returns (n_accept, next_tok), tensors that the next call overwrites.
+        Called once before it is captured (it makes its scratch)."""
         if self.queries is None:
             raise ValueError("verify goes with a verification step (queries=Q)")
         need = C.csa2_verify_drafts_workspace_bytes(self.B, target.shape[1])
-        with self._filling(stream):
-            if self.ws_verify is None or self.ws_verify.numel() < need:
-                self.ws_verify = C.workspace(need, self.out.device)
-            if self.n_accept is None:
-                self.n_accept = torch.zeros(self.B, dtype=torch.int32, device=self.out.device)
-                self.next_tok = torch.zeros(self.B, dtype=torch.int32, device=self.out.device)
-        C.csa2_verify_drafts(target, tokens, q_off, u, r, self.n_accept, self.next_tok, self.ws_verify, draft=draft,
+        if not self.ws_verify or self.ws_verify[-1].numel() < need:
+            self.ws_verify.append(self._scratch(need, stream))
+        C.csa2_verify_drafts(target, tokens, q_off, u, r, self.n_accept, self.next_tok, self.ws_verify[-1], draft=draft,
                              out_tokens=out_tokens, seq_len_in=seq_len, seq_len_out=seq_len, stream=stream)
         return self.n_accept, self.next_tok
 
@@ -427,14 +434,12 @@ class DecodeStep:
         to its Full layer's ``FullCache.acc`` (``csa2_attn_weights``), layer by
         layer.  Verification steps pass q_off, and n_accept (from ``verify``)
         to count only the candidates that stand; seq_len may then be the
-        lengths without the rejected ones."""
+        lengths without the rejected ones.  Called once before it is captured."""
         if (self.queries is None) != (q_off is None):
             raise ValueError("q_off goes with (and only with) a verification step")
         nq = self.topk[0].shape[0]
         if self.ws_weights is None:
-            with self._filling(stream):
-                self.ws_weights = C.workspace(C.csa2_attn_weights_workspace_bytes(self.B, nq, self.k),
-                                              self.out.device)
+            self.ws_weights = self._scratch(C.csa2_attn_weights_workspace_bytes(self.B, nq, self.k), stream)
         for layer, _, f, _ in self.plan:
             if caches[f].acc is None:
                 raise ValueError("accumulate needs FullCache.acc")
@@ -461,7 +466,7 @@ class DecodeStep:
 
     def device_flags(self) -> int:
         flags = C.device_status(self.ws_full)
-        extra = [p.ws for p in self.pairs] + [self.ws_verify, self.ws_weights]
+        extra = [p.ws for p in self.pairs] + [*self.ws_verify, self.ws_weights]
         flat = []
         for w in self.ws_re + self.ws_attn:
             flat.extend(w if isinstance(w, list) else [w])

@@ -1,6 +1,9 @@
 """The calls that follow a step, without a GPU: host-side checks of the C
 entry points and the binding (bad arguments are refused before any launch),
 the orchestration in DecodeStep, and the plain forms the GPU tests use."""
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -204,6 +207,33 @@ def test_decode_step_orchestrates_the_calls(fake):  # noqa: F811
                                                                              torch.zeros(5), torch.zeros(2))
     with pytest.raises(ValueError, match="acc"):
         evict(FullCache(caches[0].idx, caches[0].main), caches[1], off, off, lens, i(2), 32, 16, i(2, 16), i(2), z(256))
+
+
+def test_decode_step_keeps_its_scratch(fake, monkeypatch):  # noqa: F811
+    """A captured graph goes on using the scratch that it was captured with: a larger vocabulary adds to it."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    made, real = [], C.workspace
+    need = {40: 512, 400: 4096}
+
+    def record(nbytes, device=None):
+        ws = real(nbytes, device)
+        made.append(weakref.ref(ws))
+        return ws
+
+    step = DecodeStep("F", 2, 32, 16, 8, device="cpu", concurrent=False, queries=5)
+    monkeypatch.setattr(C, "workspace", record)
+    monkeypatch.setattr(C, "csa2_verify_drafts_workspace_bytes", lambda B, V: need[V])
+    outs = []
+    for V in (40, 400, 40):
+        outs.append(step.verify(torch.zeros((5, V)), i(5), i(3), torch.zeros(5), torch.zeros(2)))
+    gc.collect()
+    assert len(made) == 2 and all(w() is not None for w in made)
+    assert fake.calls[0][1][-2] == 512 and fake.calls[1][1][-2] == 4096
+    assert outs[0][0] is outs[1][0] and outs[0][1] is outs[2][1]
+    flags = []
+    monkeypatch.setattr(C, "device_status", lambda ws, stream=None: flags.append(ws.data_ptr()) or 0)
+    step.device_flags()
+    assert {w().data_ptr() for w in made} <= set(flags)
 
 
 # ---------------------------------------------------------------------------

@@ -697,6 +697,53 @@ def test_calls_capture_and_replay():
     assert all(C.device_status(ws) == 0 for ws in wa + wb)
 
 
+def test_decode_step_scratch_is_not_made_in_a_capture():
+    """Scratch made there would be filled at the first replay only: the first verify and accumulate are plain calls."""
+    p, q, tokens, off, u, r = _problem(3, 4, 5003, 3)
+    wc = WeightCase([600, 900, 300], np.diff(off), 64, seed=4)
+    Q, V = len(tokens), 5003
+    step = DecodeStep("F", 3, 1024, 64, 64, queries=Q)
+    step.topk[0].copy_(_i32(wc.topk))
+    step.lse[0].copy_(dev(wc.lse))
+    main = C.cache(dev(wc.codes), dev(wc.scales))
+    caches = [FullCache(None, main, dev(wc.acc))]
+    tok, qo, lens, woff, layers = _i32(tokens), _i32(off), _i32(wc.lens), dev(wc.off), [{"q": wc.q.cuda()}]
+    narrow = torch.softmax(torch.randn((Q, 300), device="cuda"), 1)
+    small = _i32(np.asarray(tokens) % 300)
+
+    def verify(stream=None):
+        return step.verify(p, tok, qo, u, r, draft=q, stream=stream)
+
+    def accumulate(stream=None):
+        step.accumulate(caches, woff, lens, layers, q_off=qo, n_accept=step.n_accept, stream=stream)
+
+    def capture(call):
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s, capture_error_mode="thread_local"):
+            call()
+        return g
+
+    step.verify(narrow, small, qo, u, r)                  # a small vocabulary first: a larger one needs more scratch
+    for call in (verify, accumulate):
+        with pytest.raises(ValueError, match="capture"):
+            capture(call)
+    want = R.verify(_f64(p), _f64(q), tokens, off, _f64(u), _f64(r))
+    n, t = verify()
+    assert np.array_equal(host(n), want[0]) and np.array_equal(host(t), want[1])
+    accumulate()
+    acc = caches[0].acc.clone()
+    g = capture(lambda: (verify(), accumulate()))
+    n.fill_(-9)
+    caches[0].acc.copy_(dev(wc.acc))
+    g.replay()
+    assert np.array_equal(host(n), want[0]) and torch.equal(caches[0].acc, acc)
+    step.verify(torch.softmax(torch.randn((Q, 60000), device="cuda"), 1), tok, qo, u, r)   # the graph keeps its own
+    caches[0].acc.copy_(dev(wc.acc))
+    g.replay()
+    assert np.array_equal(host(n), want[0]) and torch.equal(caches[0].acc, acc) and step.device_flags() == 0
+
+
 def test_one_workspace_serves_batches_of_any_size():
     """Large and small batches in turn on one workspace: neither's scratch lies where the other counts arrivals."""
     few, many = WeightCase([900] * 3, [6] * 3, 512, seed=1), WeightCase([70] * 150, [2] * 150, 64, seed=2)
