@@ -112,6 +112,10 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   float* mine = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem)) + warp * warp_cap;  // this warp's weights
   const bool vec = (reinterpret_cast<uintptr_t>(a.acc_src) & 15) == 0;
   launch_dependents();
+  // The cluster's CTAs write into one another's shared memory, which needs all
+  // of them running: each arrives here and waits before its first such access
+  // (the first pass over the weights lies between).
+  cl.barrier_arrive();
   for (int i = tid; i < kBins; i += kEThreads) sm.hist[i] = 0;
   if (tid == 0) sm.listed = sm.gathered = 0;
   grid_wait();
@@ -123,6 +127,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
     // only the protected entries stay, or all of them
     for (int j = rank * kEThreads + tid; j < p.n; j += C * kEThreads)
       kept[j] = p.need > 0 || j < p.first ? j : m1 + (j - p.first);
+    cl.barrier_wait();
     cl.sync();  // every CTA has read the length (seq_len_out may be seq_len itself)
     if (rank == 0 && tid == 0) a.seq_len_out[b] = p.n;
     return;
@@ -205,6 +210,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
     eq += uint32_t(f.x == 0.0f) + uint32_t(f.y == 0.0f) + uint32_t(f.z == 0.0f) + uint32_t(f.w == 0.0f);
   });
   put(gt, eq);
+  cl.barrier_wait();
   share(0);
   int slot = 0;
   uint32_t left = uint32_t(p.need);
