@@ -342,6 +342,7 @@ __device__ __forceinline__ void select_segment(const void* __restrict__ in, int6
   const int s = blockIdx.x / CL;
   const uint32_t rank = CL == 1 ? 0u : sm100::cluster_ctarank();
   const int tid = threadIdx.x;
+  if (CL == 2) sm100::cluster_arrive();
   int64_t n;
   if (KIND == kSelBlockKeys) n = (int64_t(seg_eff[s]) + kBlk - 1) / kBlk;
   else if (KIND == kSelScores) n = seg_eff[s];
@@ -463,7 +464,8 @@ __device__ __forceinline__ void select_segment(const void* __restrict__ in, int6
   uint32_t total = 0, b1 = 0, need = 0, cnt = 0;
   if (CL == 2) {
     // CTA 0 finds the threshold bucket from the producer's histogram and
-    // sends it to CTA 1 (ghist is non-null whenever CL == 2)
+    // sends it to CTA 1 (ghist is non-null whenever CL == 2), which runs by now
+    sm100::cluster_wait();
     if (rank == 0) {
       present = take_hist<kHist1Bins>(ghist + int64_t(s) * kHist1Bins, hist);
       __syncthreads();
