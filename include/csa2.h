@@ -572,7 +572,9 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
 
 /* ---------------------------------------------------------------------------
  * csa2_cache_evict, csa2_cache_evict_paged -- keeps the entries of a cache
- * that carried the most attention weight, and moves them together.
+ * that carried the most attention weight, and moves them together;
+ * csa2_cache_evict_layers, csa2_cache_evict_layers_paged -- the same of
+ * several layers' caches, which keep the same entries.
  * Source: the pages have no counterpart of eviction (their caches only grow);
  * the rows moved are the main KV and indexer K of [V41] section
  * "三个方向一起压小缓存".
@@ -585,6 +587,16 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
  * rows of positions 0 .. n-1; no other destination byte is written (zero the
  * accumulators' destination once: new entries' accumulators start at zero).
  * Positions held from before (pools, selections) refer to the source.
+ * Layers whose selections come from one candidate pool (a step's Full layers,
+ * of which only the first scans) know an entry by its position: they have to
+ * keep the same ones, and are evicted by one csa2_cache_evict_layers call.
+ * It ranks by the sum of the layers' accumulators (fp32, layer 0 first; equal
+ * acc_src pointers count once) and moves every layer's rows and accumulators.
+ * Its main_src .. acc_dst are host arrays of n_layers (1..64) entries, read
+ * during the call; idx_src and idx_dst may be NULL (no indexer caches).  The
+ * layers share row offsets or page tables; the rows that every layer has count
+ * as the caches' capacity.  Layers that share accumulators may share their
+ * destination too; no other memory may belong to two layers.
  *   main_src, main_dst  main-KV caches;  idx_src, idx_dst  indexer-K caches,
  *              or both with codes and scales NULL
  *   acc_src    [src rows] fp32;  acc_dst [dst rows] fp32
@@ -618,6 +630,20 @@ csa2_status csa2_cache_evict_paged(csa2_mxfp4_cache main_src, csa2_mxfp4_cache i
                                    const int32_t* dst_pages, int dst_max_pages, int page_rows, int32_t* kept_out,
                                    int32_t* seq_len_out, int B, int max_len, int max_keep, int first, int last,
                                    void* workspace, size_t workspace_bytes, void* stream);
+csa2_status csa2_cache_evict_layers(int n_layers, const csa2_mxfp4_cache* main_src, const csa2_mxfp4_cache* idx_src,
+                                    const float* const* acc_src, const int64_t* src_row_off, const int32_t* seq_len,
+                                    const int32_t* keep, const csa2_mxfp4_cache* main_dst,
+                                    const csa2_mxfp4_cache* idx_dst, float* const* acc_dst, const int64_t* dst_row_off,
+                                    int32_t* kept_out, int32_t* seq_len_out, int B, int max_len, int max_keep,
+                                    int first, int last, void* workspace, size_t workspace_bytes, void* stream);
+csa2_status csa2_cache_evict_layers_paged(int n_layers, const csa2_mxfp4_cache* main_src,
+                                          const csa2_mxfp4_cache* idx_src, const float* const* acc_src,
+                                          const int32_t* pages, int max_pages, const int32_t* seq_len,
+                                          const int32_t* keep, const csa2_mxfp4_cache* main_dst,
+                                          const csa2_mxfp4_cache* idx_dst, float* const* acc_dst,
+                                          const int32_t* dst_pages, int dst_max_pages, int page_rows,
+                                          int32_t* kept_out, int32_t* seq_len_out, int B, int max_len, int max_keep,
+                                          int first, int last, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, returns the status word of `workspace` in *flags
  * (CSA2_DEV_* bits) and clears it.  Returns CSA2_ERR_DEVICE_CHECK when any

@@ -97,6 +97,9 @@ def lib():
             "csa2_cache_evict": (I, [Cache, Cache, P, P, P, P, Cache, Cache, P, P, P, P, I, I, I, I, I, P, Z, P]),
             "csa2_cache_evict_paged": (I, [Cache, Cache, P, P, I, P, P, Cache, Cache, P, P, I, I, P, P, I, I, I, I, I,
                                            P, Z, P]),
+            "csa2_cache_evict_layers": (I, [I, P, P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, P, Z, P]),
+            "csa2_cache_evict_layers_paged": (I, [I, P, P, P, P, I, P, P, P, P, P, P, I, I, P, P, I, I, I, I, I, P, Z,
+                                                  P]),
             "csa2_device_status": (I, [P, P, C.POINTER(C.c_uint32)]),
             "csa2_status_string": (C.c_char_p, [I]),
             "csa2_last_error": (C.c_char_p, []),
@@ -631,3 +634,39 @@ def csa2_cache_evict(main_src, idx_src, acc_src, src, seq_len, keep, max_len, ma
     else:
         _launch(fn, tensors, stream, main_src, i_src, ac, _row_off(fn, src, B), sl, kp, main_dst, i_dst, ad,
                 _row_off(fn, dst, B), *tail)
+
+
+def csa2_cache_evict_layers(main_src, idx_src, acc_src, src, seq_len, keep, max_len, max_keep, main_dst, idx_dst,
+                            acc_dst, dst, kept, seq_len_out, ws, first=0, last=0, stream=None):
+    """csa2_cache_evict of several layers, which keep the same entries: the best by the sum of their accumulators.
+    main_src, idx_src, acc_src, main_dst, idx_dst, acc_dst: one per layer (idx_src / idx_dst: lists, or None)."""
+    paged = isinstance(src, PageTable)
+    fn = "csa2_cache_evict_layers_paged" if paged else "csa2_cache_evict_layers"
+    if paged != isinstance(dst, PageTable) or (paged and src.page_rows != dst.page_rows):
+        raise Csa2Error(-1, fn, "source and destination must both be row offsets, or page tables of one page size")
+    n = len(main_src)
+    idx_src, idx_dst = (x if x is not None else [None] * n for x in (idx_src, idx_dst))
+    if n < 1 or any(len(x) != n for x in (idx_src, acc_src, main_dst, idx_dst, acc_dst)):
+        raise Csa2Error(-1, fn, "one cache and one accumulator per layer on each side expected")
+    if any((a is None) != (b is None) for a, b in zip(idx_src, idx_dst)):
+        raise Csa2Error(-1, fn, "idx_src and idx_dst go together")
+    B = seq_len.shape[0]
+    wp, wn = _ws(ws)
+    # an accumulator per row that all caches of a side hold
+    n_src = min(c.rows for c in (*main_src, *idx_src) if c is not None)
+    n_dst = min(c.rows for c in (*main_dst, *idx_dst) if c is not None)
+    none = MXFP4Cache(None, None, 0)
+    caches = lambda cs: (MXFP4Cache * n)(*(none if c is None else c for c in cs))  # noqa: E731
+    accs = lambda name, ts, rows: (C.c_void_p * n)(*(_arg(fn, name, t, "f32", rows) for t in ts))  # noqa: E731
+    head = (n, caches(main_src), caches(idx_src), accs("acc_src", acc_src, n_src))
+    there = (caches(main_dst), caches(idx_dst), accs("acc_dst", acc_dst, n_dst))
+    sl, kp = _arg(fn, "seq_len", seq_len, "i32", B), _arg(fn, "keep", keep, "i32", B)
+    tail = (_arg(fn, "kept", kept, "i32", B * max_keep), _arg(fn, "seq_len_out", seq_len_out, "i32", B), B,
+            int(max_len), int(max_keep), int(first), int(last), wp, wn)
+    tensors = (*acc_src, seq_len, keep, *acc_dst, kept, seq_len_out, ws, src.pages if paged else src,
+               dst.pages if paged else dst, *_cache_tensors(*main_src, *idx_src, *main_dst, *idx_dst))
+    if paged:
+        _launch(fn, tensors, stream, *head, _pages(fn, src, B), src.max_pages, sl, kp, *there, _pages(fn, dst, B),
+                dst.max_pages, src.page_rows, *tail)
+    else:
+        _launch(fn, tensors, stream, *head, _row_off(fn, src, B), sl, kp, *there, _row_off(fn, dst, B), *tail)

@@ -972,6 +972,114 @@ bool caches_overlap(const csa2_mxfp4_cache& s, const csa2_mxfp4_cache& d, size_t
   return overlap(s.codes, size_t(s.rows) * codes, d.codes, size_t(d.rows) * codes) ||
          overlap(s.scales, size_t(s.rows) * scales, d.scales, size_t(d.rows) * scales);
 }
+bool rows_overlap(const csa2_mxfp4_cache& main_a, const csa2_mxfp4_cache& idx_a, const csa2_mxfp4_cache& main_b,
+                  const csa2_mxfp4_cache& idx_b) {
+  return caches_overlap(main_a, main_b, kMainCodeBytes, kMainScaleBytes) ||
+         (idx_a.codes && idx_b.codes && caches_overlap(idx_a, idx_b, kIdxCodeBytes, kIdxScaleBytes));
+}
+
+// The caches and accumulators of the layers that keep the same entries.
+struct EvictLayers {
+  int n;
+  const csa2_mxfp4_cache *main_src, *idx_src;  // idx_src, idx_dst null: no indexer caches
+  const float* const* acc_src;
+  const csa2_mxfp4_cache *main_dst, *idx_dst;
+  float* const* acc_dst;
+};
+
+// `base` holds what the layers share; its source is completed here (max_len
+// host bound, row offsets or the page tables of both sides).
+csa2_status evict_impl(const char* fn, const EvictLayers& l, EvictArgs base, const int64_t* src_row_off,
+                       const int32_t* pages, int max_pages, const int32_t* seq_len, int64_t max_len, int page_rows,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  const csa2_mxfp4_cache none{nullptr, nullptr, 0};
+  EvictArgs a[kMaxEvictLayers];
+  int64_t srows = INT64_MAX, drows = INT64_MAX;  // rows that every layer has
+  for (int i = 0; i < l.n; ++i) {
+    a[i] = base;
+    a[i].main_src = l.main_src[i], a[i].idx_src = l.idx_src ? l.idx_src[i] : none;
+    a[i].main_dst = l.main_dst[i], a[i].idx_dst = l.idx_dst ? l.idx_dst[i] : none;
+    a[i].acc_src = l.acc_src[i], a[i].acc_dst = l.acc_dst[i];
+    const int64_t s = cache_rows(a[i].main_src, a[i].idx_src), d = cache_rows(a[i].main_dst, a[i].idx_dst);
+    int shift = 0;
+    if (pages && (!pages_ok(pages, page_rows, max_pages, a[i].main_src.rows, s, &shift) ||
+                  !pages_ok(base.dst_pages, page_rows, base.dst_max_pages, a[i].main_dst.rows, d, &shift)))
+      return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
+    base.dst_shift = shift;
+    srows = srows < s ? srows : s;
+    drows = drows < d ? drows : d;
+  }
+  for (int i = 0; i < l.n; ++i) {
+    a[i].src = pages ? paged_desc(pages, base.dst_shift, max_pages, seq_len, max_len, srows)
+                     : SegDesc{src_row_off, 0, seq_len, max_len, srows};
+    a[i].dst_shift = base.dst_shift;
+    a[i].dst_rows = drows;
+    const csa2_status rc = evict_args(fn, a[i], a[i].acc_src, max_len, workspace, workspace_bytes);
+    if (rc != CSA2_OK) return rc;
+  }
+  const size_t sbytes = size_t(srows) * 4, dbytes = size_t(drows) * 4;
+  for (int i = 0; i < l.n; ++i) {
+    for (int j = 0; j < l.n; ++j) {
+      // a layer's destination may be memory of its own source's pool only with
+      // page tables, and of another layer's source or destination never (its
+      // accumulators may be shared as a whole: they get the same values)
+      const bool own_pool = pages && i == j;
+      if (!own_pool && rows_overlap(a[i].main_src, a[i].idx_src, a[j].main_dst, a[j].idx_dst))
+        return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": source and destination overlap");
+      const bool one_acc = a[i].acc_src == a[j].acc_src;
+      if (!(pages && one_acc) && overlap(a[i].acc_src, sbytes, a[j].acc_dst, dbytes))
+        return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": source and destination overlap");
+      if (i < j && (rows_overlap(a[i].main_dst, a[i].idx_dst, a[j].main_dst, a[j].idx_dst) ||
+                    (!(one_acc && a[i].acc_dst == a[j].acc_dst) && overlap(a[i].acc_dst, dbytes, a[j].acc_dst, dbytes))))
+        return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": the destinations of two layers overlap");
+    }
+  }
+  return launch_evict(a, l.n, static_cast<cudaStream_t>(stream));
+}
+
+EvictArgs evict_base(const int32_t* keep, int32_t* kept_out, int32_t* seq_len_out, int B, int max_keep, int first,
+                     int last, void* workspace) {
+  EvictArgs a{};
+  a.keep = keep;
+  a.kept = kept_out;
+  a.seq_len_out = seq_len_out;
+  a.max_keep = max_keep;
+  a.first = first;
+  a.last = last;
+  a.B = B;
+  a.status = static_cast<uint32_t*>(workspace);
+  return a;
+}
+
+csa2_status evict_rows(const char* fn, const EvictLayers& l, const int64_t* src_row_off, const int32_t* seq_len,
+                       const int64_t* dst_row_off, EvictArgs base, int max_len, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (base.B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (base.B == 0) return CSA2_OK;
+  if (!src_row_off || !dst_row_off) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  base.dst_row_off = dst_row_off;
+  return evict_impl(fn, l, base, src_row_off, nullptr, 0, seq_len, max_len, 0, workspace, workspace_bytes, stream);
+}
+
+csa2_status evict_pages(const char* fn, const EvictLayers& l, const int32_t* pages, int max_pages,
+                        const int32_t* seq_len, const int32_t* dst_pages, int dst_max_pages, int page_rows,
+                        EvictArgs base, int max_len, void* workspace, size_t workspace_bytes, void* stream) {
+  if (base.B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (base.B == 0) return CSA2_OK;
+  if (!pages || !dst_pages) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
+  base.dst_pages = dst_pages;
+  base.dst_max_pages = dst_max_pages;
+  return evict_impl(fn, l, base, nullptr, pages, max_pages, seq_len, max_len, page_rows, workspace, workspace_bytes,
+                    stream);
+}
+
+csa2_status layers_ok(const char* fn, const EvictLayers& l) {
+  if (l.n < 1 || l.n > kMaxEvictLayers)
+    return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": 1 to 64 layers are taken");
+  if (!l.main_src || !l.main_dst || !l.acc_src || !l.acc_dst || (l.idx_src == nullptr) != (l.idx_dst == nullptr))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  return CSA2_OK;
+}
 }  // namespace
 
 csa2_status csa2_cache_evict(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
@@ -980,21 +1088,10 @@ csa2_status csa2_cache_evict(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src
                              const int64_t* dst_row_off, int32_t* kept_out, int32_t* seq_len_out, int B, int max_len,
                              int max_keep, int first, int last, void* workspace, size_t workspace_bytes,
                              void* stream) {
-  const char* fn = "csa2_cache_evict";
-  if (B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
-  if (B == 0) return CSA2_OK;
-  if (!src_row_off || !dst_row_off) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
-  const int64_t srows = cache_rows(main_src, idx_src), drows = cache_rows(main_dst, idx_dst);
-  const EvictArgs a{main_src, idx_src, main_dst, idx_dst, acc_src, acc_dst,
-                    SegDesc{src_row_off, 0, seq_len, max_len, srows}, keep, dst_row_off, nullptr, 0, 0, drows,
-                    kept_out, seq_len_out, max_keep, first, last, B, static_cast<uint32_t*>(workspace)};
-  const csa2_status rc = evict_args(fn, a, acc_src, max_len, workspace, workspace_bytes);
-  if (rc != CSA2_OK) return rc;
-  if (caches_overlap(main_src, main_dst, kMainCodeBytes, kMainScaleBytes) ||
-      (idx_src.codes && caches_overlap(idx_src, idx_dst, kIdxCodeBytes, kIdxScaleBytes)) ||
-      overlap(acc_src, size_t(srows) * 4, acc_dst, size_t(drows) * 4))
-    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": source and destination overlap");
-  return launch_evict(a, static_cast<cudaStream_t>(stream));
+  return evict_rows("csa2_cache_evict", EvictLayers{1, &main_src, &idx_src, &acc_src, &main_dst, &idx_dst, &acc_dst},
+                    src_row_off, seq_len, dst_row_off,
+                    evict_base(keep, kept_out, seq_len_out, B, max_keep, first, last, workspace), max_len, workspace,
+                    workspace_bytes, stream);
 }
 
 csa2_status csa2_cache_evict_paged(csa2_mxfp4_cache main_src, csa2_mxfp4_cache idx_src, const float* acc_src,
@@ -1003,21 +1100,44 @@ csa2_status csa2_cache_evict_paged(csa2_mxfp4_cache main_src, csa2_mxfp4_cache i
                                    const int32_t* dst_pages, int dst_max_pages, int page_rows, int32_t* kept_out,
                                    int32_t* seq_len_out, int B, int max_len, int max_keep, int first, int last,
                                    void* workspace, size_t workspace_bytes, void* stream) {
-  const char* fn = "csa2_cache_evict_paged";
-  if (B < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
-  if (B == 0) return CSA2_OK;
-  const int64_t srows = cache_rows(main_src, idx_src), drows = cache_rows(main_dst, idx_dst);
-  int shift = 0;
-  if (!pages_ok(pages, page_rows, max_pages, main_src.rows, srows, &shift) ||
-      !pages_ok(dst_pages, page_rows, dst_max_pages, main_dst.rows, drows, &shift))
-    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
-  const EvictArgs a{main_src, idx_src, main_dst, idx_dst, acc_src, acc_dst,
-                    paged_desc(pages, shift, max_pages, seq_len, max_len, srows), keep, nullptr, dst_pages, shift,
-                    dst_max_pages, drows, kept_out, seq_len_out, max_keep, first, last, B,
-                    static_cast<uint32_t*>(workspace)};
-  const csa2_status rc = evict_args(fn, a, acc_src, max_len, workspace, workspace_bytes);
+  return evict_pages("csa2_cache_evict_paged",
+                     EvictLayers{1, &main_src, &idx_src, &acc_src, &main_dst, &idx_dst, &acc_dst}, pages, max_pages,
+                     seq_len, dst_pages, dst_max_pages, page_rows,
+                     evict_base(keep, kept_out, seq_len_out, B, max_keep, first, last, workspace), max_len, workspace,
+                     workspace_bytes, stream);
+}
+
+csa2_status csa2_cache_evict_layers(int n_layers, const csa2_mxfp4_cache* main_src, const csa2_mxfp4_cache* idx_src,
+                                    const float* const* acc_src, const int64_t* src_row_off, const int32_t* seq_len,
+                                    const int32_t* keep, const csa2_mxfp4_cache* main_dst,
+                                    const csa2_mxfp4_cache* idx_dst, float* const* acc_dst, const int64_t* dst_row_off,
+                                    int32_t* kept_out, int32_t* seq_len_out, int B, int max_len, int max_keep,
+                                    int first, int last, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_cache_evict_layers";
+  const EvictLayers l{n_layers, main_src, idx_src, acc_src, main_dst, idx_dst, acc_dst};
+  const csa2_status rc = layers_ok(fn, l);
   if (rc != CSA2_OK) return rc;
-  return launch_evict(a, static_cast<cudaStream_t>(stream));
+  return evict_rows(fn, l, src_row_off, seq_len, dst_row_off,
+                    evict_base(keep, kept_out, seq_len_out, B, max_keep, first, last, workspace), max_len, workspace,
+                    workspace_bytes, stream);
+}
+
+csa2_status csa2_cache_evict_layers_paged(int n_layers, const csa2_mxfp4_cache* main_src,
+                                          const csa2_mxfp4_cache* idx_src, const float* const* acc_src,
+                                          const int32_t* pages, int max_pages, const int32_t* seq_len,
+                                          const int32_t* keep, const csa2_mxfp4_cache* main_dst,
+                                          const csa2_mxfp4_cache* idx_dst, float* const* acc_dst,
+                                          const int32_t* dst_pages, int dst_max_pages, int page_rows,
+                                          int32_t* kept_out, int32_t* seq_len_out, int B, int max_len, int max_keep,
+                                          int first, int last, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  const char* fn = "csa2_cache_evict_layers_paged";
+  const EvictLayers l{n_layers, main_src, idx_src, acc_src, main_dst, idx_dst, acc_dst};
+  const csa2_status rc = layers_ok(fn, l);
+  if (rc != CSA2_OK) return rc;
+  return evict_pages(fn, l, pages, max_pages, seq_len, dst_pages, dst_max_pages, page_rows,
+                     evict_base(keep, kept_out, seq_len_out, B, max_keep, first, last, workspace), max_len, workspace,
+                     workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -20,6 +20,10 @@
 // (an entry is 4 bytes): the passes compare floats, and the ordered write
 // scans the flags of 128 positions at once, four counts to a register.
 //
+// The Full layers of a step that select in one candidate pool know an entry by
+// its position, so all of them keep the same ones: one selection, by the sum of
+// the layers' weights (added as they are read), and a move per layer.
+//
 // k_evict_move copies the rows: a CTA takes a run of destination rows, so its
 // writes are contiguous and every CTA moves the same amount whatever the
 // selection.  It is bound by HBM (a row is 272 + 68 + 4 bytes read and
@@ -103,14 +107,38 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v, int) {
   return v;
 }
 
-__global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int warp_cap) {
+// What an entry is ranked by: its accumulator, or the sum of its accumulators
+// in several layers (fp32, in their order; NaN in one of them makes it NaN).
+struct OneLayer {
+  __device__ __forceinline__ float4 add4(float4 f, int64_t, bool) const { return f; }
+  __device__ __forceinline__ float add(float f, int64_t) const { return f; }
+};
+struct MoreLayers {
+  int n;
+  const float* acc[kMaxEvictLayers - 1];  // behind EvictArgs::acc_src
+  __device__ __forceinline__ float4 add4(float4 f, int64_t row, bool vec) const {
+    for (int l = 0; l < n; ++l) {
+      const float* src = acc[l] + row;
+      const float4 x = vec ? __ldg(reinterpret_cast<const float4*>(src))
+                           : make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
+      f.x += x.x, f.y += x.y, f.z += x.z, f.w += x.w;
+    }
+    return f;
+  }
+  __device__ __forceinline__ float add(float f, int64_t row) const {
+    for (int l = 0; l < n; ++l) f += __ldg(acc[l] + row);
+    return f;
+  }
+};
+
+template <class L>
+__global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, L layers, int warp_cap, bool vec) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
   cg::cluster_group cl = cg::this_cluster();
   const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* mine = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem)) + warp * warp_cap;  // this warp's weights
-  const bool vec = (reinterpret_cast<uintptr_t>(a.acc_src) & 15) == 0;
   launch_dependents();
   // The cluster's CTAs write into one another's shared memory, which needs all
   // of them running: each arrives here and waits before its first such access
@@ -141,6 +169,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
   const float* base = a.src.pages ? nullptr : a.acc_src + a.src.row_off[b];
   // (a step never crosses a page)
   auto step_at = [&](int q0) { return base ? base + q0 : a.acc_src + seg_row(a.src, b, q0, a.status); };
+  auto one = [&](const float* src) { return layers.add(__ldg(src), src - a.acc_src); };
   // The whole warp over its part, 4 consecutive positions per lane and step:
   // fn(position, four weights), from the accumulators on (kBatch steps' loads
   // in flight) or from shared memory as far as it goes.  Entries that do not
@@ -166,6 +195,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
           const float* src = step_at(q0 + i * kStep) + 4 * lane;
           f[i] = vec ? __ldg(reinterpret_cast<const float4*>(src))
                      : make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
+          f[i] = layers.add4(f[i], src - a.acc_src, vec);
         }
       }
 #pragma unroll
@@ -259,7 +289,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
         });
       } else {
         for (int q = w0 + lane; q < w1; q += 32) {
-          const float y = q < wc ? mine[q - w0] : __ldg(step_at(q / kStep * kStep) + q % kStep);
+          const float y = q < wc ? mine[q - w0] : one(step_at(q / kStep * kStep) + q % kStep);
           if (q >= m0 && q < m1 && !(y >= 0.0f)) fn(rank_key(y));
         }
       }
@@ -416,7 +446,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, int war
       const float* src = q0 + h * kStep < w1 ? step_at(q0 + h * kStep) : nullptr;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        f[h][i] = q0 + h * kStep + 32 * i + lane < w1 ? __ldg(src + 32 * i + lane) : 0.0f;
+        f[h][i] = q0 + h * kStep + 32 * i + lane < w1 ? one(src + 32 * i + lane) : 0.0f;
     }
     emit(q0, f[0]);
     if (q0 + kStep < w1) emit(q0 + kStep, f[1]);
@@ -481,9 +511,8 @@ __global__ void __launch_bounds__(kMThreads, 8) k_evict_move(EvictArgs a) {
   if (d >= 0) a.acc_dst[d] = __ldg(a.acc_src + s);
 }
 
-}  // namespace
-
-csa2_status launch_evict(const EvictArgs& a, cudaStream_t st) {
+template <class L>
+csa2_status launch_select(const EvictArgs& a, const L& layers, bool vec, cudaStream_t st) {
   // CTAs per sequence: one for every 8192 positions while the clusters of all
   // sequences run at once.  The CTAs of a cluster share a GPC, so a B200's 148
   // SMs hold fewer clusters than 148 / C: kActive[C], as its occupancy query
@@ -498,13 +527,33 @@ csa2_status launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int64_t fit = (int64_t(226) * 1024 - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
   const int warp_cap = int(std::min(part, fit)) * kStep;
   const size_t smem = sizeof(SelSmem) + size_t(warp_cap) * 4 * kEWarps;
-  if (smem > 48 * 1024) cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (C > 8) cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  launch_k_cluster(k_evict_select, dim3(C, a.B), dim3(kEThreads), smem, st, C, a, warp_cap);
-  const csa2_status rc = check_launch("csa2_cache_evict");
-  if (rc != CSA2_OK) return rc;
-  launch_k(k_evict_move, dim3(unsigned((int64_t(a.max_keep) + kMRows - 1) / kMRows), unsigned(a.B)), dim3(kMThreads), 0, st, a);
+  if (smem > 48 * 1024)
+    cudaFuncSetAttribute(k_evict_select<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (C > 8) cudaFuncSetAttribute(k_evict_select<L>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  launch_k_cluster(k_evict_select<L>, dim3(C, a.B), dim3(kEThreads), smem, st, C, a, layers, warp_cap, vec);
   return check_launch("csa2_cache_evict");
+}
+
+}  // namespace
+
+csa2_status launch_evict(const EvictArgs* a, int n, cudaStream_t st) {
+  // accumulators that layers share count once
+  MoreLayers more{};
+  bool vec = aligned16(a[0].acc_src);
+  for (int l = 1; l < n; ++l) {
+    bool seen = a[l].acc_src == a[0].acc_src;
+    for (int m = 0; m < more.n; ++m) seen |= a[l].acc_src == more.acc[m];
+    if (seen) continue;
+    more.acc[more.n++] = a[l].acc_src;
+    vec = vec && aligned16(a[l].acc_src);
+  }
+  csa2_status rc = more.n ? launch_select(a[0], more, vec, st) : launch_select(a[0], OneLayer{}, vec, st);
+  for (int l = 0; l < n && rc == CSA2_OK; ++l) {
+    launch_k(k_evict_move, dim3(unsigned((int64_t(a[l].max_keep) + kMRows - 1) / kMRows), unsigned(a[l].B)),
+             dim3(kMThreads), 0, st, a[l]);
+    rc = check_launch("csa2_cache_evict");
+  }
+  return rc;
 }
 
 }  // namespace csa2

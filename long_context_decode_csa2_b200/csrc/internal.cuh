@@ -325,6 +325,8 @@ struct EvictArgs {
   int max_keep, first, last, B;
   uint32_t* status;
 };
-csa2_status launch_evict(const EvictArgs& a, cudaStream_t st);
+// n layers (equal but for their caches and accumulators), one selection.
+constexpr int kMaxEvictLayers = 64;
+csa2_status launch_evict(const EvictArgs* a, int n, cudaStream_t st);
 
 }  // namespace csa2

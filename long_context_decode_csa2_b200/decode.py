@@ -49,24 +49,46 @@ from . import csa2 as C
 @dataclass
 class FullCache:
     """One Full layer's caches; acc ([rows] fp32, optional) accumulates the
-    attention weight of the entries (zero for entries not yet attended)."""
+    attention weight of the entries (zero for entries not yet attended).
+
+    layers: how many Full layers' caches hold the same entries at the same
+    positions because their selections come from one candidate pool
+    (``DecodeStep.accumulate`` notes it); these are evicted together."""
 
     idx: C.MXFP4Cache
     main: C.MXFP4Cache
     acc: torch.Tensor | None = None
+    layers: int = 1
 
 
-def evict(src: FullCache, dst: FullCache, src_rows, dst_rows, seq_len, keep, max_len: int, max_keep: int, kept,
-          seq_len_out, ws, first: int = 0, last: int = C.WINDOW, stream=None):
+def evict(src, dst, src_rows, dst_rows, seq_len, keep, max_len: int, max_keep: int, kept, seq_len_out, ws,
+          first: int = 0, last: int = C.WINDOW, stream=None):
     """Cuts every sequence of ``src`` to keep[b] entries (the first ``first``,
     the last ``last`` and the most attended others) and copies them, in order,
-    to ``dst``.  src_rows / dst_rows: row offsets, or page tables of one pool.
-    kept [B, max_keep] receives the kept positions, seq_len_out [B] their
-    number.  ``ws``: csa2_cache_evict_workspace_bytes(B, max_len) bytes."""
-    if src.acc is None or dst.acc is None:
+    to ``dst``.  src, dst: a FullCache, or those of all Full layers of a step
+    (a later Full layer selects inside the first one's pool, whose ids are
+    positions, so all keep the same entries: the most attended ones of all
+    layers together).  src_rows / dst_rows: row offsets, or page tables of one
+    pool.  kept [B, max_keep] receives the kept positions, seq_len_out [B]
+    their number.  ``ws``: csa2_cache_evict_workspace_bytes(B, max_len) bytes."""
+    srcs, dsts = ([c] if isinstance(c, FullCache) else list(c) for c in (src, dst))
+    if len(srcs) != len(dsts) or not srcs:
+        raise ValueError("eviction takes as many destination caches as source caches, at least one")
+    if any(c.acc is None for c in srcs + dsts):
         raise ValueError("eviction ranks entries by FullCache.acc: both caches need one")
-    C.csa2_cache_evict(src.main, src.idx, src.acc, src_rows, seq_len, keep, max_len, max_keep, dst.main, dst.idx,
-                       dst.acc, dst_rows, kept, seq_len_out, ws, first=first, last=last, stream=stream)
+    if max(c.layers for c in srcs) > len(srcs):
+        raise ValueError(f"these entries belong to {max(c.layers for c in srcs)} Full layers, which select in one pool: "
+                         "evict all of their caches in one call")
+    if len(srcs) == 1:
+        (s,), (d,) = srcs, dsts
+        C.csa2_cache_evict(s.main, s.idx, s.acc, src_rows, seq_len, keep, max_len, max_keep, d.main, d.idx, d.acc,
+                           dst_rows, kept, seq_len_out, ws, first=first, last=last, stream=stream)
+    else:
+        side = lambda cs: ([c.main for c in cs], [c.idx for c in cs], [c.acc for c in cs])  # noqa: E731
+        C.csa2_cache_evict_layers(*side(srcs), src_rows, seq_len, keep, max_len, max_keep, *side(dsts), dst_rows, kept,
+                                  seq_len_out, ws, first=first, last=last, stream=stream)
+    for s, d in zip(srcs, dsts):
+        d.layers = s.layers
 
 
 def layer_plan(pattern: str, full_rescan: bool = False):
@@ -440,9 +462,13 @@ class DecodeStep:
         nq = self.topk[0].shape[0]
         if self.ws_weights is None:
             self.ws_weights = self._scratch(C.csa2_attn_weights_workspace_bytes(self.B, nq, self.k), stream)
+        # Full layers that select in another one's pool keep their entries at the same positions
+        n_full = 1 + max(f for _, _, f, _ in self.plan)
+        pooled = any(m == "F" and act == "reindex" for _, m, _, act in self.plan)
         for layer, _, f, _ in self.plan:
             if caches[f].acc is None:
                 raise ValueError("accumulate needs FullCache.acc")
+            caches[f].layers = n_full if pooled else 1
             C.csa2_attn_weights(layers[layer]["q"], caches[f].main, seq_row_off, seq_len, self.topk[layer],
                                 self.lse[layer], self.sm_scale, caches[f].acc, self.ws_weights, q_off=q_off,
                                 n_accept=n_accept, stream=stream)

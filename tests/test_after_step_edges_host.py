@@ -1,0 +1,143 @@
+"""Edges of the calls that follow a step, without a GPU: what they refuse, and
+how the step's orchestration keeps the layers' caches in step."""
+import ctypes
+
+import pytest
+import torch
+
+from long_context_decode_csa2_b200 import csa2 as C
+from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
+from tests.test_binding_host import FakeStream, fake  # noqa: F401  (fixture)
+
+GIB = 1 << 30
+
+
+def _i(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+def _z(*s):
+    return torch.zeros(s, dtype=torch.uint8)
+
+
+def _full_cache(rows=64, acc=True):
+    return FullCache(C.cache(_z(rows, 64), _z(rows, 4)), C.cache(_z(rows, 256), _z(rows, 16)),
+                     torch.zeros(rows) if acc else None)
+
+
+# ---------------------------------------------------------------------------
+# eviction of several layers
+# ---------------------------------------------------------------------------
+
+def _layers(n=2, paged=False, dst=lambda i, plane: (8 + i) * GIB + (plane << 26), src=lambda i, plane: (1 + i) * GIB + (plane << 26),
+            acc_src=None, acc_dst=None, idx=True, rows=1024, B=2, idx_dst=True, page_rows=512):
+    caches = lambda at, a, b: (C.MXFP4Cache * max(n, 1))(*(C.MXFP4Cache(at(i, a), at(i, b), rows) for i in range(n)))  # noqa: E731
+    ptrs = lambda v, at: (ctypes.c_void_p * max(n, 1))(*(v or [at(i, 4) for i in range(n)]))  # noqa: E731
+    ms, md, xs, xd = caches(src, 0, 1), caches(dst, 0, 1), caches(src, 2, 3), caches(dst, 2, 3)
+    head = [n, ms, xs if idx else None, ptrs(acc_src, src)]
+    there = [md, xd if idx and idx_dst else None, ptrs(acc_dst, dst)]
+    tail = [GIB >> 1, GIB >> 1, B, 512, 256, 0, 0, GIB >> 1, 255, None]   # the workspace is one byte short
+    fake_at = GIB >> 1
+    if paged:
+        return C.lib().csa2_cache_evict_layers_paged(*head, fake_at, 4, fake_at, fake_at, *there, fake_at, 4, page_rows, *tail)
+    return C.lib().csa2_cache_evict_layers(*head, fake_at, fake_at, fake_at, *there, fake_at, *tail)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_evict_layers_refuses(paged):
+    """A call that is sound but for its workspace answers -3; what is wrong is refused before that, or with it."""
+    call = lambda **kw: _layers(paged=paged, **kw)  # noqa: E731
+    assert call() == -3 and call(n=1) == -3 and call(n=64) == -3 and call(idx=False) == -3
+    assert call(n=0) == -2 and call(n=65) == -2 and call(n=-1) == -2 and call(idx_dst=False) == -1
+    assert call(B=0) == 0 and call(B=-1) == -1 and call(rows=1001) == -1
+    if paged:
+        assert call(page_rows=500) == -1
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_evict_layers_refuses_memory_of_two_layers(paged, monkeypatch):
+    """Overlaps are looked for once everything else is sound: with a workspace, and none of these calls launches."""
+    src, dst = (lambda i, plane: (1 + i) * GIB + (plane << 26)), (lambda i, plane: (8 + i) * GIB + (plane << 26))
+
+    def call(ws_bytes=256, **kw):
+        L = C.lib()
+        name = "csa2_cache_evict_layers" + ("_paged" if paged else "")
+        real = getattr(L, name)
+        with monkeypatch.context() as m:
+            m.setattr(L, name, lambda *a: real(*a[:-2], ws_bytes, a[-1]))
+            return _layers(paged=paged, **kw)
+
+    assert call(dst=lambda i, plane: 8 * GIB + (plane << 26)) == -1                    # one destination for both
+    assert call(dst=lambda i, plane: src(1 - i, plane)) == -1                          # each other's source
+    assert call(dst=lambda i, plane: dst(i, plane) if plane != 3 else dst(0, 3)) == -1  # indexer scales alone
+    assert call(acc_dst=[dst(0, 4)] * 2) == -1                                         # two layers' weights to one place
+    assert call(acc_src=[src(0, 4)] * 2, acc_dst=[dst(0, 4), dst(0, 4) + 8]) == -1
+    assert call(acc_dst=[src(1, 4), dst(1, 4)]) == -1
+    if not paged:
+        assert call(dst=src) == -1
+        assert call(acc_src=[src(0, 4)] * 2, acc_dst=[src(0, 4)] * 2) == -1
+    assert b"overlap" in C.lib().csa2_last_error()
+
+
+def _evict_args(n):
+    off = torch.zeros(2, dtype=torch.int64)
+    return dict(src_rows=off, dst_rows=off, seq_len=_i(2), keep=_i(2), max_len=32, max_keep=16, kept=_i(2, 16),
+                seq_len_out=_i(2), ws=_z(256))
+
+
+def test_evict_of_a_steps_layers(fake):  # noqa: F811
+    """Full layers that select in the first one's pool are evicted together; a lone one of them is refused."""
+    args = _evict_args(2)
+    src, dst = [_full_cache() for _ in range(2)], [_full_cache() for _ in range(2)]
+    evict(src[0], dst[0], **args)                        # nothing says that it has company: a cache of its own
+    step = DecodeStep("FUFR", 2, 32, 16, 8, device="cpu", concurrent=False)
+    layers = [dict(q=torch.zeros((2, 16, 512), dtype=torch.bfloat16)) for _ in range(4)]
+    step.accumulate(src, args["src_rows"], args["seq_len"], layers)
+    fake.calls.clear()
+    for lone in (src[0], [src[1]]):
+        with pytest.raises(ValueError, match="2 Full layers"):
+            evict(lone, dst[0], **args)
+    assert not fake.calls
+    evict(src, dst, **args)
+    (name, a), = fake.calls
+    assert name == "csa2_cache_evict_layers" and a[0] == 2
+    for f in range(2):
+        assert a[1][f].codes == src[f].main.codes and a[2][f].scales == src[f].idx.scales
+        assert a[3][f] == src[f].acc.data_ptr() and a[9][f] == dst[f].acc.data_ptr()
+        assert a[7][f].scales == dst[f].main.scales and a[8][f].codes == dst[f].idx.codes
+    with pytest.raises(ValueError, match="2 Full layers"):
+        evict(dst[1], src[1], **args)                    # what was evicted together goes on together
+    pt = C.PageTable(_i(2, 1), 512)
+    evict(src, dst, **{**args, "src_rows": pt, "dst_rows": pt})
+    assert fake.calls[-1][0] == "csa2_cache_evict_layers_paged"
+    with pytest.raises(ValueError, match="as many"):
+        evict(src, dst[:1], **args)
+    with pytest.raises(ValueError, match="at least one"):
+        evict([], [], **args)
+    with pytest.raises(ValueError, match="acc"):
+        evict(src, [dst[0], _full_cache(acc=False)], **args)
+    # layers that scan for themselves keep what they like
+    DecodeStep("FUFR", 2, 32, 16, 8, device="cpu", concurrent=False, full_rescan=True).accumulate(
+        src, args["src_rows"], args["seq_len"], layers)
+    evict(src[1], dst[1], **args)
+    assert fake.calls[-1][0] == "csa2_cache_evict"
+
+
+def test_evict_layers_binding_checks(fake):  # noqa: F811
+    src, dst = [_full_cache() for _ in range(2)], [_full_cache() for _ in range(2)]
+    off = torch.zeros(2, dtype=torch.int64)
+    pt = C.PageTable(_i(2, 1), 512)
+    base = dict(main_src=[c.main for c in src], idx_src=[c.idx for c in src], acc_src=[c.acc for c in src], src=off,
+                seq_len=_i(2), keep=_i(2), max_len=32, max_keep=16, main_dst=[c.main for c in dst],
+                idx_dst=[c.idx for c in dst], acc_dst=[c.acc for c in dst], dst=off, kept=_i(2, 16), seq_len_out=_i(2),
+                ws=_z(256))
+    for change in (dict(src=pt), dict(dst=pt), dict(src=pt, dst=C.PageTable(_i(2, 1), 1024)), dict(idx_dst=None),
+                   dict(main_src=[src[0].main]), dict(acc_dst=[dst[0].acc]), dict(kept=_i(2, 15)),
+                   dict(acc_src=[src[0].acc, torch.zeros(63)]), dict(acc_dst=[dst[0].acc, torch.zeros(64).double()]),
+                   dict(main_src=[], idx_src=[], acc_src=[], main_dst=[], idx_dst=[], acc_dst=[])):
+        with pytest.raises(C.Csa2Error):
+            C.csa2_cache_evict_layers(**{**base, **change})
+    assert not fake.calls
+    C.csa2_cache_evict_layers(**{**base, "idx_src": None, "idx_dst": None})
+    (_, a), = fake.calls
+    assert a[2][0].codes is None and a[8][1].codes is None

@@ -2,11 +2,19 @@
 forms: what a batch, a distribution or a second use can bring that the tests of
 each call's ordinary range do not."""
 import numpy as np
+import math
+
+import numpy as np
 import pytest
 import torch
 
+import oracle
+import synth.workloads as W
 from long_context_decode_csa2_b200 import csa2 as C
-from tests.test_gpu_after_step import EvictCase
+from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
+from tests import _after_step as R
+from tests._gpu import check_attention, dev, host
+from tests.test_gpu_after_step import EvictCase, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -27,6 +35,159 @@ def test_evict_short_sequences_in_wide_clusters(max_len, page):
     for _ in range(20):
         got = c.call(keep, 400, max_len=max_len)
         assert torch.equal(got["kept"], want["kept"]) and torch.equal(got["len"], want["len"])
+
+
+def _by_rows(rows, planes, g):
+    return [torch.randint(0, 256, (rows, p.shape[1]), dtype=torch.uint8, device="cuda", generator=g) for p in planes]
+
+
+@pytest.mark.parametrize("page", [0, 512])
+@pytest.mark.parametrize("n,kind,share,shift,lens", [
+    (2, "mixed", 0.3, 0, [0, 1, 9, 513, 9000]), (3, "ties", 0.6, 3, [700, 4097]), (4, "odd", 0.9, 0, [5000, 129]),
+    (2, "odd", 0.97, 1, [70001]), (3, "mixed", 0.5, 0, [900001, 64]), (5, "zeros", 0.4, 2, [3000])])
+def test_evict_layers_matches_the_plain_form(n, kind, share, shift, lens, page):
+    """Every layer keeps the entries with the largest sum of the layers' weights, whatever each layer's own are."""
+    cases = [EvictCase(lens, kind, page, seed=7 * l + n) for l in range(n)]
+    c0, B, first, last = cases[0], len(lens), 3, 70
+    keep = [int(L * share) for L in lens]
+    max_keep, rows, drows = max(max(keep), 1), c0.rows, c0.drows
+    g = torch.Generator(device="cuda").manual_seed(n)
+    src = [[p.clone() for p in c.planes] for c in cases]
+    dst = src if page else [_by_rows(drows, c.planes, g) for c in cases]
+    before = [[p.clone() for p in d] for d in dst]
+    acc = [dev(np.concatenate([np.zeros(shift, np.float32), c.acc]))[shift:] for c in cases]
+    dacc = acc if page else [torch.full((drows,), -5.0, device="cuda") for _ in cases]
+    where = (C.PageTable(dev(c0.table), page), C.PageTable(dev(c0.dtable), page)) if page else (dev(c0.off), dev(c0.doff))
+    seq_len, kept = _i32(lens), torch.full((B, max_keep), -9, dtype=torch.int32, device="cuda")
+    ws = C.workspace(C.csa2_cache_evict_workspace_bytes(B, max(lens)))
+    mains, idxs = ([C.cache(*p[i:i + 2]) for p in src] for i in (0, 2))
+    dmains, didxs = ([C.cache(*p[i:i + 2]) for p in dst] for i in (0, 2))
+    C.csa2_cache_evict_layers(mains, idxs, acc, where[0], seq_len, _i32(keep), max(lens), max_keep, dmains, didxs, dacc,
+                              where[1], kept, seq_len, ws, first=first, last=last)   # the lengths in place
+    assert C.device_status(ws) == 0
+    with np.errstate(invalid="ignore"):
+        total = cases[0].acc.copy()
+        for c in cases[1:]:
+            total = total + c.acc                            # fp32, layer by layer
+    want_acc = [c.acc.copy() if page else np.full(drows, -5.0, np.float32) for c in cases]
+    for b, L in enumerate(lens):
+        at = c0.row_of(b, np.arange(L))
+        pos = R.evict_positions(total[at], keep[b], first, last)
+        assert host(seq_len)[b] == len(pos)
+        assert np.array_equal(host(kept)[b, :len(pos)], pos) and (host(kept)[b, len(pos):] == -1).all()
+        if len(pos):
+            s, t = c0.row_of(b, pos), c0.drow_of(b, np.arange(len(pos)))
+            for l, c in enumerate(cases):
+                want_acc[l][t] = c.acc[s]
+                for p, w in zip(c.planes, before[l]):
+                    w[torch.from_numpy(t).cuda()] = p[torch.from_numpy(s).cuda()]
+    for l in range(n):
+        assert all(torch.equal(w, d) for w, d in zip(before[l], dst[l])), l
+        assert np.array_equal(host(dacc[l]).view(np.int32), want_acc[l].view(np.int32)), l
+
+
+def test_evict_layers_with_shared_accumulators():
+    """Layers that add to the same accumulators: they count once and are moved once for all."""
+    c = EvictCase([3000, 700], "odd", seed=1)
+    one = c.call([1500, 200], 1500, first=2, last=30)
+    acc, dacc, w = dev(c.acc), torch.full((c.drows,), -5.0, device="cuda"), C.workspace(256)
+    kept, ln = torch.zeros((2, 1500), dtype=torch.int32, device="cuda"), _i32([0, 0])
+    dst = [[p.clone() for p in c.dplanes] for _ in range(3)]
+    C.csa2_cache_evict_layers([C.cache(*c.planes[:2])] * 3, None, [acc] * 3, dev(c.off), _i32(c.lens), _i32([1500, 200]),
+                              3000, 1500, [C.cache(*d[:2]) for d in dst], None, [dacc] * 3, dev(c.doff), kept, ln, w,
+                              first=2, last=30)
+    assert C.device_status(w) == 0
+    assert torch.equal(kept, one["kept"]) and torch.equal(ln, one["len"])
+    assert np.array_equal(host(dacc).view(np.int32), host(one["acc"]).view(np.int32))
+    for d in dst:
+        assert all(torch.equal(a, b) for a, b in zip(d[:2], one["dst"][:2]))
+        assert all(torch.equal(a, b) for a, b in zip(d[2:], c.dplanes[2:]))   # no indexer cache was given
+
+
+@pytest.mark.parametrize("page", [0, 512])
+def test_decode_after_eviction_of_two_full_layers(page):
+    """FRUFR: the second Full layer selects inside the first one's pool on its own caches.  Its accumulators differ from
+    the first one's; after the eviction both hold the same tokens at the same positions, so that the next step agrees
+    with the oracle on the rows that stayed."""
+    pattern, P, k = "FRUFR", 64, 64
+    wl = W.DecodeWorkload("evict_two", np.array([900, 5000, 2500]), pattern, P=P, k=k, needles=8)
+    layers_h = [W.layer_inputs_host(wl, l) for l in range(len(pattern))]
+    fulls = wl.full_layers()
+    caches_h = [W.full_cache_host(wl, f, layers_h[f]["q_codes"], layers_h[f]["q_scales"]) for f in fulls]
+    names = ("idx_codes", "idx_scales", "main_codes", "main_scales")
+    off, lens, B = caches_h[0]["seq_row_off"], wl.lengths.astype(np.int32), 3
+    rows = caches_h[0]["idx_codes"].shape[0]
+    keys = ("q", "q_codes", "q_scales", "w", "win", "win_scale", "win_len")
+    layers = [{n: dev(L[n]) for n in keys} for L in layers_h]
+    left = [300, 1250, 2000]
+    if page:
+        # source rows as pages of a pool, the destination's pages behind them
+        need, dneed = [(int(n) + page - 1) // page for n in lens], [(n + page - 1) // page for n in left]
+        table, dtable = np.full((B, max(need)), -1, np.int32), np.full((B, max(need)), -1, np.int32)
+        perm = np.random.default_rng(2).permutation(sum(need) + sum(dneed)).astype(np.int32)
+        o = 0
+        for b in range(B):
+            table[b, :need[b]], o = perm[o:o + need[b]], o + need[b]
+            dtable[b, :dneed[b]], o = perm[o:o + dneed[b]], o + dneed[b]
+        row_of = lambda b, t: table[b, t // page].astype(np.int64) * page + t % page  # noqa: E731
+        drow_of = lambda b, t: dtable[b, t // page].astype(np.int64) * page + t % page  # noqa: E731
+        src_rows, dst_rows, rows = C.PageTable(dev(table), page), C.PageTable(dev(dtable), page), len(perm) * page
+    else:
+        cap = [(n + 7) // 8 * 8 for n in left]
+        doff = np.concatenate([[0], np.cumsum(cap)[:-1]]).astype(np.int64)
+        row_of, drow_of = lambda b, t: off[b] + t, lambda b, t: doff[b] + t
+        src_rows, dst_rows = dev(off), dev(doff)
+    planes = []
+    for c in caches_h:
+        by = []
+        for n in names:
+            p = np.zeros((rows, c[n].shape[1]), np.uint8)
+            for b in range(B):
+                p[row_of(b, np.arange(lens[b]))] = c[n][off[b]:off[b] + lens[b]]
+            by.append(dev(p))
+        planes.append(by)
+    full = lambda p, r: FullCache(C.cache(*p[:2]), C.cache(*p[2:]), torch.zeros(r, device="cuda"))  # noqa: E731
+    src = [full(p, rows) for p in planes]
+    step = DecodeStep(pattern, B, 5120, P, k)
+    d_len = dev(lens)
+    step.run(src, src_rows, d_len, layers)
+    step.accumulate(src, src_rows, d_len, layers)
+    acc = [host(c.acc) for c in src]
+    if page:
+        dplanes, dst = planes, src
+    else:
+        dplanes = [[torch.zeros((sum(cap), p.shape[1]), dtype=torch.uint8, device="cuda") for p in ps] for ps in planes]
+        dst = [full(p, sum(cap)) for p in dplanes]
+    kept = torch.zeros((B, 2000), dtype=torch.int32, device="cuda")
+    ws = C.workspace(C.csa2_cache_evict_workspace_bytes(B, 5120))
+    with pytest.raises(ValueError, match="2 Full layers"):
+        evict(src[1], dst[1], src_rows, dst_rows, d_len, _i32(left), 5120, 2000, kept, d_len, ws)
+    evict(src, dst, src_rows, dst_rows, d_len, _i32(left), 5120, 2000, kept, d_len, ws, first=4)
+    assert host(d_len).tolist() == left and C.device_status(ws) == 0
+    small, alone = [{n: np.zeros((6000, caches_h[0][n].shape[1]), np.uint8) for n in names} for _ in fulls], []
+    soff = np.array([0, 1000, 3000], np.int64)
+    for b in range(B):
+        at = row_of(b, np.arange(lens[b]))
+        pos = R.evict_positions(acc[0][at] + acc[1][at], left[b], 4, 128)
+        assert np.array_equal(host(kept)[b, :left[b]], pos)
+        alone += [not np.array_equal(pos, R.evict_positions(a[at], left[b], 4, 128)) for a in acc]
+        for f, c in enumerate(caches_h):
+            for i, n in enumerate(names):
+                small[f][n][soff[b]:soff[b] + left[b]] = c[n][off[b] + pos]
+                got = host(dplanes[f][i])
+                assert np.array_equal(got[drow_of(b, np.arange(left[b]))], c[n][off[b] + pos]), (b, f, n)
+            t = drow_of(b, np.arange(left[b]))
+            assert np.array_equal(host(dst[f].acc)[t], acc[f][row_of(b, pos)])
+    assert any(alone)                                     # a layer by itself would have kept others
+    wd = W.DecodeWorkload("evict_two_d", np.array(left), pattern, P=P, k=k)
+    nl_h = [W.layer_inputs_host(wd, l) for l in range(len(pattern))]
+    nl = [{n: dev(L[n]) for n in keys} for L in nl_h]
+    step.run(dst, dst_rows, d_len, nl)
+    ref = oracle.decode_step(pattern, small, soff, np.array(left, np.int32), nl_h, P, k, 1 / math.sqrt(512))
+    for l in range(len(pattern)):
+        assert np.array_equal(host(step.topk[l]), ref["topk"][l]), l
+        check_attention(host(step.out[l]), ref["out"][l])
+    assert step.device_flags() == 0
 
 
 # ---------------------------------------------------------------------------
