@@ -291,16 +291,18 @@ __device__ __forceinline__ void find_segment(const double* part, int nseg, float
     total += sm.scan[w];
     lastpos = max(lastpos, sm.lastpos[w]);
   }
-  const double want = double(r) * total;
+  const double want = r >= 1.0f ? double(INFINITY) : double(r) * total;  // (from 1 on: the last weighted token)
   double c = __shfl_up_sync(0xffffffffu, incl, 1);
   c = before + (lane == 0 ? 0.0 : c);
   // this thread's first segment that passes, and what lies before it (or
-  // before segment lastpos, which is taken where none passes)
+  // before segment lastpos, which is taken where none passes).  Only segments
+  // with a weight pass: c comes from the scan's grouping of the sums, `total`
+  // from another, so behind the last weight c may lie an ulp above it.
   int hit = -1;
   double base = 0.0, base_last = 0.0;
   auto step = [&](int s, double x) {
     if (s == lastpos) base_last = c;
-    if (hit < 0 && c + x > want) hit = s, base = c;
+    if (hit < 0 && x > 0.0 && c + x > want) hit = s, base = c;
     c += x;
   };
 #pragma unroll

@@ -14,9 +14,41 @@ from long_context_decode_csa2_b200 import csa2 as C
 from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
 from tests import _after_step as R
 from tests._gpu import check_attention, dev, host
-from tests.test_gpu_after_step import EvictCase, _i32
+from tests.test_gpu_after_step import EvictCase, _check_verify, _i32, _verify
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# verification
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("V", [5003, 131072, 300001])
+def test_verify_draws_the_last_token_with_a_weight(V):
+    """Filtered distributions end in zeros.  From r = 1 on the draw is the last token with a weight, whatever the sums
+    round to; just below, it is the plain form's."""
+    n = 100 if V > 200000 else 400
+    g = torch.Generator(device="cuda").manual_seed(V)
+    p = torch.softmax(2.5 * torch.randn((n, V), device="cuda", generator=g), 1)
+    end = torch.randint(1, V, (n,), device="cuda", generator=g)
+    end[: n // 4] = torch.randint(1, min(V, 3000), (n // 4,), device="cuda", generator=g)
+    p[torch.arange(V, device="cuda")[None] >= end[:, None]] = 0
+    p[::3] *= (torch.rand((len(p[::3]), V), device="cuda", generator=g) < 0.01)   # few tokens stand
+    p[torch.arange(n), end - 1] = 1e-3 * torch.rand(n, device="cuda", generator=g) + 1e-9
+    u, off, tokens = torch.zeros(n, device="cuda"), list(range(n + 1)), [0] * n
+    for r in (1.0, 1.5, float("inf")):
+        got = _verify(p, None, tokens, off, u, torch.full((n,), r, device="cuda"))
+        assert torch.equal(got["t"].long(), end - 1) and got["flags"] == 0, r
+    _check_verify(p, None, tokens, off, u, torch.full((n,), 1 - 2.0 ** -24, device="cuda"))
+    _check_verify(p, None, tokens, off, u, torch.rand(n, device="cuda", generator=g))
+    # drawn from a residual: rejected at candidate 1, which the target never takes
+    q = p * (0.2 + torch.rand(p.shape, device="cuda", generator=g))
+    q[torch.arange(n), end - 1] = 0
+    p2, q2 = (torch.stack([x, x], 1).reshape(2 * n, V) for x in (p, q))
+    got = _verify(p2, q2, [0, V - 1] * n, list(range(0, 2 * n + 1, 2)), torch.zeros(2 * n, device="cuda"),
+                  torch.ones(n, device="cuda"))
+    want = torch.where(end == V, 1, 0)                       # (a draft at V - 1 stands where the target has it)
+    assert torch.equal(got["n"].long(), want) and torch.equal(got["t"].long(), end - 1) and got["flags"] == 0
 
 
 # ---------------------------------------------------------------------------
