@@ -546,8 +546,8 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
  *              queries of a sequence count, the ones that csa2_verify_drafts
  *              let stand (NULL: all; a negative number counts as 0)
  *   acc        [main_kv.rows] fp32, one accumulator per cache row, read and
- *              written.  The accumulator of a new entry starts at zero: keep
- *              it zero behind the sequences' ends
+ *              written.  The accumulator of a new entry starts at zero:
+ *              csa2_acc_clear where its row may have carried another entry
  *   weights_out [Q][k] fp32 or NULL
  *   workspace  csa2_attn_weights_workspace_bytes(B, Q, k); one that is
  *              large enough may serve calls of any B, Q and k in turn
@@ -571,6 +571,31 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
                                     size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * csa2_acc_clear, csa2_acc_clear_paged -- accumulators of appended entries set
+ * to zero.
+ * Source: part of the accumulation above (no counterpart on the pages).
+ * A row can have carried another entry before: one behind the end of a cache
+ * that was evicted into a second time, one of a page that another sequence
+ * gave back, one of a rejected candidate.  The appends do not know the
+ * accumulators, so whoever appends clears them: positions len_from[b] ..
+ * len_to[b]-1 of every sequence (none where len_to[b] <= len_from[b]; a
+ * negative len_from counts as 0).
+ *   acc        [rows] fp32, rows the capacity of the caches
+ *   seq_row_off [B] int64 (or pages, as in the paged calls)
+ *   len_from, len_to  [B] int32: the lengths before and after the append
+ *   workspace  csa2_acc_clear_workspace_bytes(B); another call's workspace
+ *              serves as well (only the status word is used)
+ * A sequence that does not fit the rows is left out, entries of a page outside
+ * the cache are not written (CSA2_DEV_ROW_LAYOUT for both).
+ * ------------------------------------------------------------------------- */
+size_t csa2_acc_clear_workspace_bytes(int B);
+csa2_status csa2_acc_clear(float* acc, int64_t rows, const int64_t* seq_row_off, const int32_t* len_from,
+                           const int32_t* len_to, int B, void* workspace, size_t workspace_bytes, void* stream);
+csa2_status csa2_acc_clear_paged(float* acc, int64_t rows, const int32_t* pages, int page_rows, int max_pages,
+                                 const int32_t* len_from, const int32_t* len_to, int B, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * csa2_cache_evict, csa2_cache_evict_paged -- keeps the entries of a cache
  * that carried the most attention weight, and moves them together;
  * csa2_cache_evict_layers, csa2_cache_evict_layers_paged -- the same of
@@ -584,8 +609,9 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
  * ranks below every number).  Kept entries keep their order: kept_out[b][j]
  * is the source position of the destination's entry j.  Rows of the main
  * cache, the indexer cache and the accumulators are copied to the destination
- * rows of positions 0 .. n-1; no other destination byte is written (zero the
- * accumulators' destination once: new entries' accumulators start at zero).
+ * rows of positions 0 .. n-1; no other destination byte is written.  Behind
+ * them accumulators keep what they were (another entry's, where the rows have
+ * been used before): csa2_acc_clear when entries are appended there.
  * Positions held from before (pools, selections) refer to the source.
  * Layers whose selections come from one candidate pool (a step's Full layers,
  * of which only the first scans) know an entry by its position: they have to

@@ -93,6 +93,9 @@ def lib():
             "csa2_attn_weights_workspace_bytes": (Z, [I, I, I]),
             "csa2_attn_weights": (I, [P, Cache, P, P, P, P, P, I, P, F, P, P, I, I, P, Z, P]),
             "csa2_attn_weights_paged": (I, [P, Cache, P, I, I, P, P, P, P, I, P, F, P, P, I, I, P, Z, P]),
+            "csa2_acc_clear_workspace_bytes": (Z, [I]),
+            "csa2_acc_clear": (I, [P, I64, P, P, P, I, P, Z, P]),
+            "csa2_acc_clear_paged": (I, [P, I64, P, I, I, P, P, I, P, Z, P]),
             "csa2_cache_evict_workspace_bytes": (Z, [I, I]),
             "csa2_cache_evict": (I, [Cache, Cache, P, P, P, P, Cache, Cache, P, P, P, P, I, I, I, I, I, P, Z, P]),
             "csa2_cache_evict_paged": (I, [Cache, Cache, P, P, I, P, P, Cache, Cache, P, P, I, I, P, P, I, I, I, I, I,
@@ -597,6 +600,28 @@ def csa2_attn_weights(q, main_kv, seq_row_off, seq_len, topk, lse, sm_scale, acc
         _launch(fn, tensors, stream, qp, main_kv, _pages(fn, pt, B), pt.page_rows, pt.max_pages, *rest)
     else:
         _launch(fn, tensors, stream, qp, main_kv, _row_off(fn, seq_row_off, B), *rest)
+
+
+def csa2_acc_clear_workspace_bytes(B):
+    return lib().csa2_acc_clear_workspace_bytes(B)
+
+
+def csa2_acc_clear(acc, seq_row_off, len_from, len_to, ws, rows=None, stream=None):
+    """acc of positions len_from[b] .. len_to[b]-1 of every sequence = 0.  seq_row_off: [B] offsets or a PageTable;
+    rows: capacity of the caches (None: acc has one element per row)."""
+    paged = isinstance(seq_row_off, PageTable)
+    fn = "csa2_acc_clear_paged" if paged else "csa2_acc_clear"
+    B = len_to.shape[0]
+    rows = acc.numel() if rows is None else int(rows)
+    wp, wn = _ws(ws)
+    ap = _arg(fn, "acc", acc, "f32", rows)
+    rest = (_arg(fn, "len_from", len_from, "i32", B), _arg(fn, "len_to", len_to, "i32", B), B, wp, wn)
+    tensors = (acc, seq_row_off.pages if paged else seq_row_off, len_from, len_to, ws)
+    if paged:
+        _launch(fn, tensors, stream, ap, rows, _pages(fn, seq_row_off, B), seq_row_off.page_rows, seq_row_off.max_pages,
+                *rest)
+    else:
+        _launch(fn, tensors, stream, ap, rows, _row_off(fn, seq_row_off, B), *rest)
 
 
 def csa2_cache_evict_workspace_bytes(B, max_len):

@@ -939,6 +939,47 @@ csa2_status csa2_attn_weights_paged(const uint16_t* q, csa2_mxfp4_cache main_kv,
 }
 
 // ---------------------------------------------------------------------------
+size_t csa2_acc_clear_workspace_bytes(int B) {
+  (void)B;
+  return kStatusBytes;
+}
+
+namespace {
+csa2_status clear_impl(const char* fn, float* acc, const SegDesc& sd, const int32_t* len_from, int B, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!acc || !len_from || !sd.len || !workspace) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": workspace must be 256-byte aligned");
+  if (workspace_bytes < kStatusBytes) return fail(CSA2_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  launch_clear(ClearArgs{acc, sd, len_from, B, static_cast<uint32_t*>(workspace)}, static_cast<cudaStream_t>(stream));
+  return check_launch(fn);
+}
+}  // namespace
+
+csa2_status csa2_acc_clear(float* acc, int64_t rows, const int64_t* seq_row_off, const int32_t* len_from,
+                           const int32_t* len_to, int B, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_acc_clear";
+  if (B < 0 || rows < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (B == 0) return CSA2_OK;
+  if (!seq_row_off) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
+  return clear_impl(fn, acc, SegDesc{seq_row_off, 0, len_to, INT32_MAX, rows}, len_from, B, workspace, workspace_bytes,
+                    stream);
+}
+
+csa2_status csa2_acc_clear_paged(float* acc, int64_t rows, const int32_t* pages, int page_rows, int max_pages,
+                                 const int32_t* len_from, const int32_t* len_to, int B, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const char* fn = "csa2_acc_clear_paged";
+  if (B < 0 || rows < 0) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+  if (B == 0) return CSA2_OK;
+  int shift = 0;
+  if (!pages_ok(pages, page_rows, max_pages, rows, rows, &shift))
+    return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad page table or page size");
+  return clear_impl(fn, acc, paged_desc(pages, shift, max_pages, len_to, INT32_MAX, rows), len_from, B, workspace,
+                    workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
 size_t csa2_cache_evict_workspace_bytes(int B, int max_len) {
   (void)B, (void)max_len;
   return kStatusBytes;

@@ -307,6 +307,16 @@ struct WeightArgs {
 };
 void launch_weights(const WeightArgs& a, cudaStream_t st);
 
+// Accumulators of new entries back to zero.
+struct ClearArgs {
+  float* acc;           // [cache rows]
+  SegDesc sd;           // rows of sequence b; its length is where the new entries end
+  const int32_t* from;  // [B] where they begin
+  int B;
+  uint32_t* status;
+};
+void launch_clear(const ClearArgs& a, cudaStream_t st);
+
 // Eviction by accumulated weight: the kept positions of every sequence, then
 // their rows moved to the destination.
 struct EvictArgs {

@@ -421,6 +421,23 @@ __global__ void __launch_bounds__(kAThreads) k_accumulate(WeightArgs a) {
                                                      int(len * (blockIdx.y + 1) / gridDim.y));
 }
 
+// Zeroes the accumulators of positions from[b] .. to[b]-1 of every sequence.
+// A decode step clears at most one entry per sequence (a launch); a bulk append
+// streams 4 bytes per entry.
+constexpr int kCThreads = 256;
+
+__global__ void __launch_bounds__(kCThreads) k_clear(ClearArgs a) {
+  const int b = blockIdx.x;
+  launch_dependents();
+  grid_wait();
+  const int64_t to = seg_len_checked(a.sd, b, blockIdx.y == 0 && threadIdx.x == 0 ? a.status : nullptr);
+  for (int64_t t = max(a.from[b], 0) + int64_t(blockIdx.y) * kCThreads + threadIdx.x; t < to;
+       t += int64_t(gridDim.y) * kCThreads) {
+    const int64_t row = entry_row(a.sd, b, t, a.status);
+    if (row >= 0) a.acc[row] = 0.0f;
+  }
+}
+
 template <int kTiles>
 void launch_tiles(const WeightArgs& a, int64_t ctas, cudaStream_t st) {
   constexpr int kSlots = Cfg<kTiles>::kRows * Cfg<kTiles>::kWarps;  // of a CTA at a time
@@ -431,6 +448,11 @@ void launch_tiles(const WeightArgs& a, int64_t ctas, cudaStream_t st) {
 }
 
 }  // namespace
+
+void launch_clear(const ClearArgs& a, cudaStream_t st) {
+  const int S = std::max(1, std::min(64, 2 * num_sms() / a.B));
+  launch_k(k_clear, dim3(a.B, S), dim3(kCThreads), 0, st, a);
+}
 
 void launch_weights(const WeightArgs& args, cudaStream_t st) {
   WeightArgs a = args;

@@ -49,7 +49,9 @@ from . import csa2 as C
 @dataclass
 class FullCache:
     """One Full layer's caches; acc ([rows] fp32, optional) accumulates the
-    attention weight of the entries (zero for entries not yet attended).
+    attention weight of the entries.  A new entry's starts at zero whatever its
+    row carried before: ratio-2 steps see to it, whoever appends entries
+    otherwise calls ``clear_acc``.
 
     layers: how many Full layers' caches hold the same entries at the same
     positions because their selections come from one candidate pool
@@ -91,6 +93,15 @@ def evict(src, dst, src_rows, dst_rows, seq_len, keep, max_len: int, max_keep: i
         d.layers = s.layers
 
 
+def clear_acc(caches, seq_row_off, len_from, len_to, ws, stream=None):
+    """Zeroes the accumulators of entries that were appended to ``caches``:
+    positions len_from[b] .. len_to[b]-1 of every sequence.  ``ws``:
+    csa2_acc_clear_workspace_bytes(B) bytes."""
+    for c in caches:
+        if c.acc is not None:
+            C.csa2_acc_clear(c.acc, seq_row_off, len_from, len_to, ws, rows=c.main.rows, stream=stream)
+
+
 def layer_plan(pattern: str, full_rescan: bool = False):
     """[(layer, mode, full_index, action)] with action in scan / reindex / reuse."""
     plan, f, seen_full = [], -1, False
@@ -124,15 +135,23 @@ class PairStream:
         self.pend_logit = torch.zeros(B, dtype=torch.float32, device=dev)
         self.pend_idx = None if projection else torch.zeros((B, C.IDX_DIM), dtype=torch.bfloat16, device=dev)
         self.tok_off = torch.arange(B + 1, dtype=torch.int64, device=dev)
+        self.new_len = torch.empty(B, dtype=torch.int32, device=dev)
         self.ws = C.workspace(C.csa2_compress_stream_workspace_bytes(B), dev)
 
     def append(self, cache: FullCache, tok: dict, seq_row_off, seq_len, update_len: bool, stream=None):
         """tok: raw [B,512] bf16, logit [B] fp32, and w_idx [512,128] fp32 or
-        idx_raw [B,128] bf16.  update_len: write the new lengths into seq_len."""
+        idx_raw [B,128] bf16.  update_len: write the new lengths into seq_len.
+        Where the cache has accumulators, those of new entries start at zero."""
+        acc = cache.acc is not None
+        new_len = self.new_len if acc else seq_len if update_len else None
         C.csa2_compress_stream(cache.main, cache.idx, tok["raw"], tok["logit"], self.tok_off, seq_row_off, seq_len,
-                               seq_len if update_len else None, self.pend_n, self.pend_raw, self.pend_logit, 1,
-                               self.ws, w_idx=tok.get("w_idx"), idx_raw=tok.get("idx_raw"), pend_idx=self.pend_idx,
-                               stream=stream)
+                               new_len, self.pend_n, self.pend_raw, self.pend_logit, 1, self.ws,
+                               w_idx=tok.get("w_idx"), idx_raw=tok.get("idx_raw"), pend_idx=self.pend_idx, stream=stream)
+        if acc:
+            clear_acc([cache], seq_row_off, seq_len, new_len, self.ws, stream=stream)
+            if update_len:
+                with torch.cuda.stream(stream):
+                    seq_len.copy_(new_len)
 
 
 class DecodeStep:
@@ -456,7 +475,8 @@ class DecodeStep:
         to its Full layer's ``FullCache.acc`` (``csa2_attn_weights``), layer by
         layer.  Verification steps pass q_off, and n_accept (from ``verify``)
         to count only the candidates that stand; seq_len may then be the
-        lengths without the rejected ones.  Called once before it is captured."""
+        lengths without the rejected ones.  Entries that the caller appended
+        (``clear_acc``) start at zero.  Called once before it is captured."""
         if (self.queries is None) != (q_off is None):
             raise ValueError("q_off goes with (and only with) a verification step")
         nq = self.topk[0].shape[0]

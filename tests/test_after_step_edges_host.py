@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from long_context_decode_csa2_b200 import csa2 as C
-from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
+from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, PairStream, clear_acc, evict
 from tests.test_binding_host import FakeStream, fake  # noqa: F401  (fixture)
 
 GIB = 1 << 30
@@ -141,3 +141,55 @@ def test_evict_layers_binding_checks(fake):  # noqa: F811
     C.csa2_cache_evict_layers(**{**base, "idx_src": None, "idx_dst": None})
     (_, a), = fake.calls
     assert a[2][0].codes is None and a[8][1].codes is None
+
+
+# ---------------------------------------------------------------------------
+# accumulators of new entries
+# ---------------------------------------------------------------------------
+
+def test_acc_clear_refuses():
+    L, at = C.lib(), GIB
+
+    def call(acc=at, rows=1024, off=at, a=at, b=at, B=2, ws=at, wn=256):
+        return L.csa2_acc_clear(acc, rows, off, a, b, B, ws, wn, None)
+
+    def paged(rows=1024, pages=at, page_rows=512, max_pages=2, B=2, wn=255):
+        return L.csa2_acc_clear_paged(at, rows, pages, page_rows, max_pages, at, at, B, at, wn, None)
+
+    assert call(wn=255) == -3 and paged() == -3
+    for bad in (dict(acc=None), dict(off=None), dict(a=None), dict(b=None), dict(ws=None), dict(ws=at + 8), dict(B=-1),
+                dict(rows=-8)):
+        assert call(**{"wn": 255, **bad}) == -1
+    for bad in (dict(rows=1000), dict(pages=None), dict(page_rows=300), dict(max_pages=0), dict(B=-1)):
+        assert paged(**bad) == -1
+    assert call(B=0) == 0 and paged(B=0) == 0
+
+
+def test_ratio2_appends_start_accumulators_at_zero(fake):  # noqa: F811
+    """Behind every append the new entries' accumulators are cleared, with the lengths before and after it; caches
+    without accumulators append as ever."""
+    off, lens = torch.zeros(2, dtype=torch.int64), torch.tensor([3, 5], dtype=torch.int32)
+    tok = dict(raw=torch.zeros((2, 512), dtype=torch.bfloat16), logit=torch.zeros(2), w_idx=torch.zeros((512, 128)))
+    pair = PairStream(2, "cpu")
+    for with_acc in (False, True):
+        for update in (False, True):
+            cache = _full_cache(acc=with_acc)
+            lens.copy_(torch.tensor([3, 5], dtype=torch.int32))
+            pair.new_len.copy_(torch.tensor([4, 5], dtype=torch.int32))     # as the library would leave it
+            fake.calls.clear()
+            pair.append(cache, tok, off, lens, update)
+            (name, a), *rest = fake.calls
+            out = pair.new_len.data_ptr() if with_acc else lens.data_ptr() if update else None
+            assert name == "csa2_compress_stream" and a[8] == lens.data_ptr() and a[9] == out
+            assert [n for n, _ in rest] == ["csa2_acc_clear"] * with_acc
+            if with_acc:
+                (_, c), = rest
+                assert c[0] == cache.acc.data_ptr() and c[1] == 64 and c[3:5] == (lens.data_ptr(), out)
+            assert lens.tolist() == ([4, 5] if with_acc and update else [3, 5])
+    fake.calls.clear()
+    clear_acc([_full_cache(), _full_cache(acc=False)], C.PageTable(_i(2, 1), 512), _i(2), lens, _z(256))
+    assert [n for n, _ in fake.calls] == ["csa2_acc_clear_paged"]
+    for bad in (dict(acc=torch.zeros(63)), dict(len_from=_i(1)), dict(len_to=torch.zeros(2))):
+        args = dict(acc=torch.zeros(64), seq_row_off=off, len_from=_i(2), len_to=lens, ws=_z(256), rows=64)
+        with pytest.raises(C.Csa2Error):
+            C.csa2_acc_clear(**{**args, **bad})

@@ -223,6 +223,133 @@ def test_decode_after_eviction_of_two_full_layers(page):
 
 
 # ---------------------------------------------------------------------------
+# accumulators of new entries
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("page", [0, 512])
+def test_acc_clear_clears_the_new_entries_only(page):
+    old, new = [0, 5, 700, 510, 9, 30, -3, 8], [1, 5, 4000, 1030, 3, 31, 6, 8]
+    B = len(old)
+    rng = np.random.default_rng(3)
+    if page:
+        need = [(max(n, 1) + page - 1) // page for n in new]
+        perm = rng.permutation(sum(need) + 2).astype(np.int32)
+        table = np.full((B, max(need)), -1, np.int32)
+        at = np.concatenate([[0], np.cumsum(need)])
+        for b in range(B):
+            table[b, :need[b]] = perm[at[b]:at[b + 1]]
+        row_of, rows = (lambda b, t: table[b, t // page].astype(np.int64) * page + t % page), len(perm) * page
+        where = C.PageTable(dev(table), page)
+    else:
+        cap = [(max(n, 1) + 7) // 8 * 8 for n in new]
+        off = np.concatenate([[0], np.cumsum(cap)[:-1]]).astype(np.int64)
+        row_of, rows, where = (lambda b, t: off[b] + t), sum(cap), dev(off)
+    acc = rng.random(rows).astype(np.float32)
+    want = acc.copy()
+    for b in range(B):
+        want[row_of(b, np.arange(max(old[b], 0), max(new[b], 0)))] = 0
+    d, ws = dev(acc), C.workspace(C.csa2_acc_clear_workspace_bytes(B))
+    C.csa2_acc_clear(d, where, _i32(old), _i32(new), ws)
+    assert np.array_equal(host(d), want) and C.device_status(ws) == 0
+    # what does not fit is left alone: a sequence that ends behind the rows, entries of a page that does not exist
+    d = dev(acc)
+    if page:
+        table[2, 1], want = 10 ** 6, acc.copy()
+        C.csa2_acc_clear(d, C.PageTable(dev(table), page), _i32(old), _i32([0] * 2 + [1300] + [0] * 5), ws)
+        want[row_of(2, np.arange(1024, 1300))] = 0
+    else:
+        want = acc
+        C.csa2_acc_clear(d, where, _i32(old), _i32([0] * 7 + [9]), ws)
+    assert C.device_status(ws) == 2 and np.array_equal(host(d), want)
+
+
+@pytest.mark.parametrize("page", [0, 512])
+def test_entries_appended_after_an_eviction_start_without_weight(page):
+    """Two caches (or two sets of a pool's pages) used in turn: what an entry's row carried before the eviction is not
+    the entry's.  A captured step appends, attends and accumulates between two evictions."""
+    import synth
+
+    lens0, left, room, k = [900, 333], [400, 100], 40, 64
+    wl = W.DecodeWorkload("recycled", np.array(lens0), "FU", P=64, k=k, ratio=2, room=room)
+    layers_h = [W.layer_inputs_host(wl, l) for l in range(2)]
+    c = W.full_cache_host(wl, 0, layers_h[0]["q_codes"], layers_h[0]["q_scales"])
+    off, B = c["seq_row_off"], 2
+    layers = [{n: dev(L[n]) for n in ("q", "q_codes", "q_scales", "w", "win", "win_scale", "win_len")} for L in layers_h]
+    names = ("idx_codes", "idx_scales", "main_codes", "main_scales")
+    planes = [dev(c[n]) for n in names]
+    if page:
+        rows = 8 * page
+        row_of = lambda tab, b, t: tab[b, t // page].astype(np.int64) * page + t % page  # noqa: E731
+        tabs = np.array([[0, 5], [3, -1]], np.int32), np.array([[2, 7], [6, -1]], np.int32)
+        pool = [torch.zeros((rows, p.shape[1]), dtype=torch.uint8, device="cuda") for p in planes]
+        for b in range(B):
+            t = np.arange(lens0[b])
+            for p, q in zip(pool, planes):
+                p[torch.from_numpy(row_of(tabs[0], b, t)).cuda()] = q[torch.from_numpy(off[b] + t).cuda()]
+        caches = [FullCache(C.cache(*pool[:2]), C.cache(*pool[2:]), torch.zeros(rows, device="cuda"))] * 2
+        where = [C.PageTable(dev(t), page) for t in tabs]
+        row = [lambda b, t, tab=tab: row_of(tab, b, t) for tab in tabs]
+    else:
+        rows = len(c["idx_codes"])
+        make = lambda ps: FullCache(C.cache(*ps[:2]), C.cache(*ps[2:]), torch.zeros(rows, device="cuda"))  # noqa: E731
+        caches = [make(planes), make([torch.zeros_like(p) for p in planes])]
+        where, row = [dev(off)] * 2, [lambda b, t: off[b] + t] * 2
+    step = DecodeStep("FU", B, 1000, 64, k, ratio=2, projection=False)
+    seq_len = _i32(lens0)
+    tok = lambda t: dict(  # noqa: E731
+        raw=dev(synth.normal_bf16(91, synth.T_RAW, t, 0, B * 512).reshape(B, 512)),
+        logit=dev(synth.normal_f32(91, synth.T_LOGITS, t, 0, B)),
+        idx_raw=dev(synth.normal_bf16(91, synth.T_IDXRAW, t, 0, B * 128).reshape(B, 128)))
+    ws, kept = C.workspace(256), torch.zeros((B, 400), dtype=torch.int32, device="cuda")
+    caches[1].acc.fill_(0.0) if page else caches[1].acc.fill_(7.0)   # the second cache has been used before
+    if page:                                                # and so have the pool's free pages
+        free = sorted(set(range(8)) - {0, 5, 3})
+        for f in free:
+            caches[0].acc[f * page:(f + 1) * page] = 7.0
+    side = 0
+    for turn in range(3):
+        cache, rows_now = caches[side], where[side]
+        if turn == 1:                                       # the graph replays the same calls
+            token = tok(0)
+            graph = step.capture([cache], rows_now, seq_len, layers, new_tokens=[token])
+        before = host(seq_len).copy()
+        for b in range(B):                                  # rows behind the end may carry anything
+            cache.acc[torch.from_numpy(row[side](b, np.arange(before[b], before[b] + 3))).cuda()] = 3.0
+        kept_acc = [host(cache.acc)[row[side](b, np.arange(before[b]))] for b in range(B)]
+        want = [np.concatenate([a, np.zeros(3, np.float32)]) for a in kept_acc]
+        for t in range(6):
+            new = tok(10 * turn + t)
+            if turn == 1:
+                for n, x in new.items():
+                    token[n].copy_(x)
+                graph.replay()
+            else:
+                step.run([cache], rows_now, seq_len, layers, new_tokens=[new])
+            step.accumulate([cache], rows_now, seq_len, layers)
+            # the entries' weights, layer by layer, in fp32
+            for l in range(2):
+                w, probe = torch.zeros((B, k), device="cuda"), torch.zeros_like(cache.acc)
+                C.csa2_attn_weights(layers[l]["q"], cache.main, rows_now, seq_len, step.topk[l], step.lse[l],
+                                    step.sm_scale, probe, step.ws_weights, weights=w)
+                for b in range(B):
+                    ids = host(step.topk[l])[b]
+                    want[b][ids[ids >= 0]] += host(w)[b][ids >= 0]
+        now = host(seq_len)
+        assert now.tolist() == [n + 3 for n in before]
+        for b in range(B):
+            got = host(cache.acc)[row[side](b, np.arange(now[b]))]
+            assert np.array_equal(got, want[b]), (turn, b)
+        if turn < 2:
+            evict(cache, caches[1 - side], rows_now, where[1 - side], seq_len, _i32(left), 1000, 400, kept, seq_len, ws,
+                  first=2, last=16)
+            pos = [R.evict_positions(want[b], left[b], 2, 16) for b in range(B)]
+            for b in range(B):
+                assert np.array_equal(host(kept)[b, :left[b]], pos[b])
+            side = 1 - side
+    assert step.device_flags() == 0 and C.device_status(ws) == 0
+
+
+# ---------------------------------------------------------------------------
 # selection by pairs of CTAs
 # ---------------------------------------------------------------------------
 
