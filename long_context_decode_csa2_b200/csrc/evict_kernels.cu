@@ -48,6 +48,7 @@ constexpr int kBatch = 4;                     // steps whose loads are in flight
 constexpr int kBins = 2048;
 constexpr int kList = kEThreads;              // entries of the threshold's bin that every CTA finishes alone
 constexpr int kMaxCluster = 16;
+constexpr int kSelSmem = 226 * 1024;          // shared memory of a selection's CTA, at most
 constexpr int kRunKeys = 8192;                // positions per CTA that are worth a CTA
 
 struct __align__(16) SelSmem {
@@ -524,11 +525,11 @@ csa2_status launch_select(const EvictArgs& a, const L& layers, bool vec, cudaStr
   // weights of a warp that stay in shared memory: its part of the run, as far as there is room
   const int64_t steps = (a.src.max_len + kStep - 1) / kStep;
   const int64_t part = ((steps + C - 1) / C + kEWarps - 1) / kEWarps;
-  const int64_t fit = (int64_t(226) * 1024 - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
+  const int64_t fit = (kSelSmem - int64_t(sizeof(SelSmem))) / (4 * kStep * kEWarps);
   const int warp_cap = int(std::min(part, fit)) * kStep;
   const size_t smem = sizeof(SelSmem) + size_t(warp_cap) * 4 * kEWarps;
-  if (smem > 48 * 1024)
-    cudaFuncSetAttribute(k_evict_select<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // (both are the kernel's, shared by all host threads: always the same values)
+  cudaFuncSetAttribute(k_evict_select<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
   if (C > 8) cudaFuncSetAttribute(k_evict_select<L>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   launch_k_cluster(k_evict_select<L>, dim3(C, a.B), dim3(kEThreads), smem, st, C, a, layers, warp_cap, vec);
   return check_launch("csa2_cache_evict");

@@ -1,13 +1,17 @@
 """Edges of the calls that follow a step, without a GPU: what they refuse, and
 how the step's orchestration keeps the layers' caches in step."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
+from long_context_decode_csa2_b200 import _build
 from long_context_decode_csa2_b200 import csa2 as C
 from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, PairStream, clear_acc, evict
-from tests.test_binding_host import FakeStream, fake  # noqa: F401  (fixture)
+from tests.test_binding_host import fake  # noqa: F401  (fixture)
 
 GIB = 1 << 30
 
@@ -193,3 +197,66 @@ def test_ratio2_appends_start_accumulators_at_zero(fake):  # noqa: F811
         args = dict(acc=torch.zeros(64), seq_row_off=off, len_from=_i(2), len_to=lens, ws=_z(256), rows=64)
         with pytest.raises(C.Csa2Error):
             C.csa2_acc_clear(**{**args, **bad})
+
+
+# ---------------------------------------------------------------------------
+# launches from several threads
+# ---------------------------------------------------------------------------
+
+_RUNTIME = r"""
+// The runtime calls of a launch, recorded: a kernel's dynamic shared memory limit and what launches ask of it.
+#include <cuda_runtime_api.h>
+#include <stdio.h>
+#define API extern "C" __attribute__((visibility("default")))
+API cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute attr, int value) {
+  if (attr == cudaFuncAttributeMaxDynamicSharedMemorySize) printf("limit %p %d\n", f, value);
+  return cudaSuccess;
+}
+API cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void**) {
+  printf("launch %p %zu\n", f, c->dynamicSmemBytes);
+  return cudaSuccess;
+}
+API cudaError_t cudaGetLastError(void) { return cudaSuccess; }
+"""
+
+_EVICT_OF_ALL_SIZES = """
+import sys
+from long_context_decode_csa2_b200 import _build
+from long_context_decode_csa2_b200 import csa2 as C
+import ctypes
+import os
+import subprocess
+import sys
+L, at, G = C.lib(), 1 << 29, 1 << 30
+cache = lambda i: (C.MXFP4Cache * 3)(*(C.MXFP4Cache((i + l) * G, (i + l) * G + (1 << 29), 1 << 20) for l in range(3)))
+for n_layers in (1, 3):
+    for max_len in (0, 1000, 20000, 60000, 120000, 300000, 700000, 1 << 20, 1 << 24):
+        for B in (1, 40):
+            src, dst = cache(1), cache(8)
+            acc = [(ctypes.c_void_p * 3)(*((i + l) * G + (3 << 28) for l in range(3))) for i in (20, 30)]
+            rc = L.csa2_cache_evict_layers(n_layers, src, None, acc[0], at, at, at, dst, None, acc[1], at, at, at, B, max_len,
+                                           64, 0, 0, at, 256, None)
+            assert rc == 0, (rc, L.csa2_last_error())
+"""
+
+
+def test_evict_sets_one_shared_memory_limit_for_all_sizes(tmp_path):
+    """The limit belongs to the kernel, not to the call: two threads that set their own sizes could launch under each
+    other's.  Recorded with a stand-in of the runtime's launch calls: one value per kernel, and every launch within it."""
+    src, lib = tmp_path / "runtime.cpp", tmp_path / "runtime.so"
+    src.write_text(_RUNTIME)
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc()))), "include")
+    subprocess.run(["g++", "-shared", "-fPIC", "-I", include, str(src), "-o", str(lib)], check=True)
+    _build.build()
+    r = subprocess.run([sys.executable, "-c", _EVICT_OF_ALL_SIZES], cwd=_build.ROOT, capture_output=True, text=True,
+                       env={**os.environ, "LD_PRELOAD": str(lib)})
+    assert r.returncode == 0, r.stderr
+    said = [line.split() for line in r.stdout.splitlines()]
+    limits = {}
+    for what, f, value in said:
+        if what == "limit":
+            limits.setdefault(f, set()).add(int(value))
+    sizes = [(f, int(v)) for what, f, v in said if what == "launch" and int(v) > 48 * 1024]
+    assert len({v for _, v in sizes}) > 3 and len({f for f, _ in sizes}) == 2     # one layer, and several
+    assert all(len(v) == 1 for v in limits.values()), limits
+    assert all(v <= max(limits[f]) for f, v in sizes)

@@ -3,6 +3,7 @@ forms: what a batch, a distribution or a second use can bring that the tests of
 each call's ordinary range do not."""
 import numpy as np
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -67,6 +68,36 @@ def test_evict_short_sequences_in_wide_clusters(max_len, page):
     for _ in range(20):
         got = c.call(keep, 400, max_len=max_len)
         assert torch.equal(got["kept"], want["kept"]) and torch.equal(got["len"], want["len"])
+
+
+def test_evict_from_two_threads():
+    """Two threads, each with its own stream, buffers and workspace, evict sequences of different lengths: neither's
+    launch depends on what the other one's asked of the kernel."""
+    cases = [EvictCase([700000], "mixed", idx=False, seed=1), EvictCase([30000], "mixed", idx=False, seed=2)]
+    want = [c.call([500], 500)["kept"] for c in cases]
+    errors = []
+
+    def work(c, want):
+        stream, ws = torch.cuda.Stream(), C.workspace(256)
+        src, dst = C.cache(*c.planes), C.cache(*[p.clone() for p in c.dplanes])
+        acc, dacc, off, doff = dev(c.acc), torch.zeros(c.drows, device="cuda"), dev(c.off), dev(c.doff)
+        n, kept, ln, L = _i32([500]), torch.zeros((1, 500), dtype=torch.int32, device="cuda"), _i32([0]), _i32(c.lens)
+        torch.cuda.synchronize()
+        try:
+            for _ in range(3000):
+                C.csa2_cache_evict(src, None, acc, off, L, n, int(c.lens[0]), 500, dst, None, dacc, doff, kept, ln, ws,
+                                   stream=stream)
+            stream.synchronize()
+            assert torch.equal(kept, want) and C.device_status(ws) == 0
+        except Exception as e:  # noqa: BLE001  (reported by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
 
 
 def _by_rows(rows, planes, g):
