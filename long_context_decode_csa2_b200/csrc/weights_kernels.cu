@@ -187,6 +187,42 @@ __device__ __forceinline__ void products(const __half (&qs)[kHq][kQStride], cons
   }
 }
 
+// The block scales of the warp's rows again, where some are 2^97 or more
+// (bytes from kBig on): those 2^64 times smaller (255 is E8M0's NaN) and the
+// others zero, or the others as they are and those zero.
+template <int kTiles>
+__device__ __forceinline__ void split_scales(const uint8_t (&raw)[16 * kTiles][kRow], float (&scale)[16 * kTiles][kBlocks],
+                                             bool big, int g, int t) {
+#pragma unroll 1
+  for (int m = 0; m < 2 * kTiles; ++m) {
+    const uint32_t word = *reinterpret_cast<const uint32_t*>(raw[8 * m + g] + kMainCodeBytes + 4 * t);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t byte = word >> (8 * i) & 255u;
+      uint32_t v = 0;
+      if (big == (byte >= kBig))
+        v = byte == 255u ? 0x7FC00000u : byte >= kBig ? (byte - 64u) << 23 : max(byte << 23, 0x00400000u);
+      scale[8 * m + g][4 * t + i] = __uint_as_float(v);
+    }
+  }
+}
+
+// First half of the products of rows with such bytes: the other blocks' sums to
+// `others`, the large ones' scales left for the second half.  Not inlined: the
+// ordinary path keeps its registers (64 x 6 candidates 22.9 against 23.4 us).
+template <int kTiles>
+__device__ __noinline__ void products_of_others(const __half (&qs)[kHq][kQStride], const uint8_t (&raw)[16 * kTiles][kRow],
+                                                float (&scale)[16 * kTiles][kBlocks], volatile float* others, int g, int t) {
+  float acc[kTiles][2][4] = {};
+  split_scales<kTiles>(raw, scale, false, g, t);
+  __syncwarp();
+  products<kTiles>(qs, raw, scale, acc, g, t);
+#pragma unroll
+  for (int r = 0; r < kTiles * 8; ++r) others[r] = acc[r >> 3][r >> 2 & 1][r & 3];
+  __syncwarp();
+  split_scales<kTiles>(raw, scale, true, g, t);
+}
+
 // Adds the weights of queries q0 .. q0 + more of sequence b, in their order, to
 // the accumulators of positions lo .. hi-1.  Every thread of the CTA; at most
 // kPer * kThreads slots.  A thread's ids are fetched two queries ahead, the
@@ -332,34 +368,26 @@ __global__ void __launch_bounds__(Cfg<kTiles>::kThreads, Cfg<kTiles>::kBlocksPer
     __syncwarp();
     const uint8_t(&raw)[kWRows][kRow] = sm.raw[warp][stage];
     // ---- block scales as floats: lane (g, t) does words t of rows g, g + 8, .. ----
-    float mul[2 * kTiles];
-    uint32_t word[2 * kTiles], big[2 * kTiles], any = 0;
+    uint32_t any = 0;
 #pragma unroll
     for (int m = 0; m < 2 * kTiles; ++m) {
-      word[m] = *reinterpret_cast<const uint32_t*>(raw[8 * m + g] + kMainCodeBytes + 4 * t);
+      const uint32_t word = *reinterpret_cast<const uint32_t*>(raw[8 * m + g] + kMainCodeBytes + 4 * t);
       static_assert(kBig == 0xE0, "the three top bits");
-      big[m] = word[m] & (word[m] << 1) & (word[m] << 2) & 0x80808080u;  // scale bytes of kBig or more
-      any |= big[m];
-      mul[m] = 1.0f;
+      any |= word & (word << 1) & (word << 2) & 0x80808080u;  // scale bytes of kBig or more
+      // 2^(byte - 127), a byte of 0 as the subnormal 2^-127
+      auto e8m0 = [](uint32_t byte) { return __int_as_float(max(int(byte << 23), 0x00400000)); };
+      *reinterpret_cast<float4*>(&sm.scale[warp][8 * m + g][4 * t]) =
+          make_float4(e8m0(word & 255u), e8m0(word >> 8 & 255u), e8m0(word >> 16 & 255u), e8m0(word >> 24));
     }
     const bool slow = __any_sync(0xffffffffu, any);
-#pragma unroll
-    for (int m = 0; m < 2 * kTiles; ++m) {
-      int sub = 0;
-      // A row with such a byte is multiplied with its scales 2^64 times smaller
-      // (blocks that this takes below 2^-127 do not matter beside one of 2^97).
-      if (slow && (__ballot_sync(0xffffffffu, big[m] != 0u) >> (4 * g) & 15u) != 0u)
-        sub = 64 << 23, mul[m] = 1.8446744073709552e19f;  // 2^64
-      // 2^(byte - 127 - sub); 255 is E8M0's NaN
-      auto e8m0 = [&](uint32_t byte) {
-        const float v = __int_as_float(max(int(byte << 23) - sub, 0x00400000));
-        return slow && byte == 255u ? __uint_as_float(0x7FC00000u) : v;
-      };
-      *reinterpret_cast<float4*>(&sm.scale[warp][8 * m + g][4 * t]) =
-          make_float4(e8m0(word[m] & 255u), e8m0(word[m] >> 8 & 255u), e8m0(word[m] >> 16 & 255u), e8m0(word[m] >> 24));
-    }
-    __syncwarp();
     float acc[kTiles][2][4] = {};
+    // Scales of 2^97 and more could overflow the fp32 sums.  Where the warp's
+    // rows hold such bytes, the other blocks are summed first and these then by
+    // themselves with scales 2^64 times smaller: both sums are as exact as the
+    // ordinary one, whatever the blocks' sizes.
+    volatile float others[kTiles * 8];  // (volatile: in memory)
+    if (slow) products_of_others<kTiles>(sm.q, raw, sm.scale[warp], others, g, t);
+    __syncwarp();
     products<kTiles>(sm.q, raw, sm.scale[warp], acc, g, t);
     __syncwarp();  // this stage is read before its next copies
     const int here = row;
@@ -371,8 +399,12 @@ __global__ void __launch_bounds__(Cfg<kTiles>::kThreads, Cfg<kTiles>::kBlocksPer
     for (int m = 0; m < 2 * kTiles; ++m) {
       w[m] = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        w[m] += expf(fmaf(acc[m >> 1][h >> 1][2 * (m & 1) + (h & 1)] * qexp[h] * mul[m], a.sm_scale, -lse[h]));
+      for (int h = 0; h < 4; ++h) {
+        const int at = 2 * (m & 1) + (h & 1);
+        float x = acc[m >> 1][h >> 1][at] * qexp[h];
+        if (slow) x = x * 1.8446744073709552e19f + others[8 * (m >> 1) + 4 * (h >> 1) + at] * qexp[h];  // 2^64
+        w[m] += expf(fmaf(x, a.sm_scale, -lse[h]));
+      }
 #pragma unroll
       for (int d = 1; d <= 2; d <<= 1) w[m] += __shfl_xor_sync(0xffffffffu, w[m], d);
     }

@@ -15,7 +15,7 @@ from long_context_decode_csa2_b200 import csa2 as C
 from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
 from tests import _after_step as R
 from tests._gpu import check_attention, dev, host
-from tests.test_gpu_after_step import EvictCase, _check_verify, _i32, _verify
+from tests.test_gpu_after_step import SM, EvictCase, WeightCase, _check_verify, _i32, _verify
 
 pytestmark = pytest.mark.gpu
 
@@ -50,6 +50,40 @@ def test_verify_draws_the_last_token_with_a_weight(V):
                   torch.ones(n, device="cuda"))
     want = torch.where(end == V, 1, 0)                       # (a draft at V - 1 stands where the target has it)
     assert torch.equal(got["n"].long(), want) and torch.equal(got["t"].long(), end - 1) and got["flags"] == 0
+
+
+# ---------------------------------------------------------------------------
+# attention weights
+# ---------------------------------------------------------------------------
+
+def _lse(c):
+    """The log-sum-exps of a case whose rows or queries were changed."""
+    for i, ids in enumerate(c.topk):
+        rows = c.row_of(c.q_seq[i], ids[ids >= 0].astype(np.int64))
+        x = c.q[i].double().numpy() @ R.dequant(c.codes[rows], c.scales[rows]).T * float(SM)
+        m = x.max(1)
+        c.lse[i] = m + np.log(np.exp(x - m[:, None]).sum(1)) + 0.2
+
+
+@pytest.mark.parametrize("lens,counts,k", [([300, 500], [2, 1], 64), ([3000, 2000], [40, 52], 1021)])
+@pytest.mark.parametrize("empty", ["codes", "query"])
+def test_weights_of_rows_with_scales_far_apart(lens, counts, k, empty):
+    """Blocks of 2^97 and more that add nothing (their codes are zero, or the query there is), beside blocks of 2^-97 to
+    2^-64 under queries that bring those to ordinary logits: the large scale must not touch the small ones."""
+    c = WeightCase(lens, counts, k, seed=3)
+    rng = np.random.default_rng(4)
+    c.scales[:] = rng.integers(30, 45, c.scales.shape)
+    c.q = (c.q.float() * 2.0 ** 85).to(torch.bfloat16)
+    big = rng.random(c.scales.shape) < 0.1
+    big[:, 5] = rng.random(len(big)) < 0.8                  # rows without a large scale among them
+    if empty == "query":
+        big[:, :5], big[:, 6:] = False, False
+        c.q[:, :, 160:192] = 0
+    else:
+        c.codes.reshape(-1, 16, 16)[big] = rng.choice(np.array([0x00, 0x80, 0x08, 0x88], np.uint8), (big.sum(), 16))
+    c.scales[big] = rng.integers(224, 255, int(big.sum()))
+    _lse(c)
+    c.check()
 
 
 # ---------------------------------------------------------------------------
