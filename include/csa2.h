@@ -552,9 +552,12 @@ csa2_status csa2_verify_drafts(const void* target, int target_type, int64_t targ
  *   workspace  csa2_attn_weights_workspace_bytes(B, Q, k); one that is
  *              large enough may serve calls of any B, Q and k in turn
  * Accuracy: relative error of a weight <= 6e-6 * (1 + A), A the largest
- * sm_scale * sum_d |q_d key_d| of its heads (fp32 sums; bf16 queries and E2M1
- * codes enter exactly, but elements below 2^-39 of a query row's largest are
- * rounded).  k is 1..2048.
+ * sm_scale * sum_d |q_d key_d| of its heads (fp32 sums; E2M1 codes enter
+ * exactly, and so do bf16 query elements down to 2^-31 of their row's largest).
+ * Smaller elements are rounded, each by at most 2^-39 of the row's largest
+ * (zero from about there on; or by 2^-151, if that is more): a logit's error
+ * grows by sm_scale * sum_d |key_d| times that over these elements.  k is
+ * 1..2048.
  * In the paged call a page id outside the cache sets CSA2_DEV_ROW_LAYOUT and
  * its entries are skipped.
  * ------------------------------------------------------------------------- */

@@ -14,9 +14,10 @@
 // rows x 16 heads (mma m16n8k16, fp32 accumulation): E2M1 codes are exact in
 // fp16, each block's E8M0 scale (converted once per group, in shared memory)
 // multiplies the block's fp32 sum, and a head's query row is scaled by a power
-// of two into [2^14, 2^15) at its largest element before it becomes fp16, so
-// every bf16 query element down to 2^-39 of the row's largest is exact and no
-// input leaves the fp16 range.  Inside a block the order of the 32 dims is
+// of two into [2^14, 2^15) at its largest element before it becomes fp16: bf16
+// elements down to 2^-31 of the row's largest are exact (their last bit is
+// 2^-24 there, fp16's smallest number), those below are rounded by at most 2^-39
+// of it, and no input leaves the fp16 range.  Inside a block the order of the 32 dims is
 // permuted (the same way for both operands) so that a lane's 8 dims are one
 // 32-bit word of codes.  Few rows: bound by the chain of dependent loads
 // (offsets, ids, rows).  Many: by instructions and shared memory reads.

@@ -15,7 +15,7 @@ from long_context_decode_csa2_b200 import csa2 as C
 from long_context_decode_csa2_b200.decode import DecodeStep, FullCache, evict
 from tests import _after_step as R
 from tests._gpu import check_attention, dev, host
-from tests.test_gpu_after_step import SM, EvictCase, WeightCase, _check_verify, _i32, _verify
+from tests.test_gpu_after_step import SM, EvictCase, WeightCase, _check_verify, _f64, _i32, _verify
 
 pytestmark = pytest.mark.gpu
 
@@ -84,6 +84,41 @@ def test_weights_of_rows_with_scales_far_apart(lens, counts, k, empty):
     c.scales[big] = rng.integers(224, 255, int(big.sum()))
     _lse(c)
     c.check()
+
+
+@pytest.mark.parametrize("lo,lens,counts,k", [(31, [300, 500], [2, 1], 64), (33, [300, 500], [2, 1], 64),
+                                              (36, [300], [1], 64), (31, [3000, 2000], [40, 52], 1021),
+                                              (34, [3000, 2000], [40, 52], 1021)])
+def test_weights_of_queries_with_a_wide_range(lo, lens, counts, k):
+    """The largest elements of each query row meet zero codes, so that elements of 2^-(lo-4) to 2^-lo of them decide.
+    Down to 2^-31 they enter exactly and the ordinary bound holds; below, each enters within 2^-39 of the largest."""
+    c = WeightCase(lens, counts, k, seed=5)
+    rng = np.random.default_rng(6)
+    shape = (len(c.q), 16, 512)
+    x = rng.integers(128, 256, shape) / 128 * np.exp2(3.0 - rng.integers(3, 8, shape)) * rng.choice([-1.0, 1.0], shape)
+    x /= 2                                                  # 2^-5 to 1
+    x[:, :, 64:96] = 2.0 ** (lo - 5)
+    c.q = torch.tensor(x).to(torch.bfloat16)
+    assert np.array_equal(_f64(c.q), x)                     # (they are bf16 numbers)
+    c.codes[:, 32:48] = rng.choice(np.array([0x00, 0x80, 0x08, 0x88], np.uint8), (c.rows, 16))
+    _lse(c)
+    top = np.abs(x).max(2)                                  # of a head's row
+    tiny = np.abs(x) < top[:, :, None] * 2.0 ** -31
+    assert tiny.any() == (lo > 31)
+    if lo == 31:
+        c.check()
+        return
+    got = c.call()
+    want, A = R.weights(x, c.codes, c.scales, c.row_of, c.topk, c.lse, float(SM), c.q_seq, c.counted(None))
+    # the ordinary roundings (tests of the call's range), and 2^-39 of the largest for every product of a small element
+    extra = np.zeros_like(want)
+    for i, ids in enumerate(c.topk):
+        key = np.abs(R.dequant(c.codes[c.row_of(c.q_seq[i], ids)], c.scales[c.row_of(c.q_seq[i], ids)]))
+        extra[i] = (2.0 ** -39 * top[i][:, None] * (tiny[i].astype(np.float64) @ key.T)).max(0) * float(SM)
+    lse = np.abs(c.lse).max(1)[:, None]
+    tol = want * (48 * 2.0 ** -23 * A + 2.0 ** -24 * (A + lse) + 2.0 ** -22 + 5 * 2.0 ** -24) + 2.0 ** -126
+    tol += want * np.expm1(extra)
+    assert got["flags"] == 0 and np.all(np.abs(host(got["w"]) - want) <= tol)
 
 
 # ---------------------------------------------------------------------------
