@@ -546,6 +546,14 @@ def _prob_rows(fn, name, t, Q, V):
     return _arg(fn, name, t[0], "prob"), _PROB_TYPES[t.dtype], t.stride(0)
 
 
+def _rows_out(fn, name, t, kind, rows, cols):
+    """_arg of an output of `rows` rows of `cols` elements, one behind the other: a flat tensor, or one whose rows have
+    exactly that many."""
+    if isinstance(t, _Tensor) and t.dim() != 1 and (t.dim() != 2 or t.shape[1] != cols):
+        raise Csa2Error(-1, fn, f"{name}: [{rows}, {cols}] expected, got {list(t.shape)}")
+    return _arg(fn, name, t, kind, rows * cols)
+
+
 def csa2_verify_drafts_workspace_bytes(B, V):
     return lib().csa2_verify_drafts_workspace_bytes(B, V)
 
@@ -592,7 +600,7 @@ def csa2_attn_weights(q, main_kv, seq_row_off, seq_len, topk, lse, sm_scale, acc
     rest = (_arg(fn, "seq_len", seq_len, "i32", B), _arg(fn, "q_off", q_off, "i32", B + 1),
             _arg(fn, "n_accept", n_accept, "i32", B), _arg(fn, "topk", topk, "i32", Q * k), k,
             _arg(fn, "lse", lse, "f32", Q * Q_HEADS), float(sm_scale), _arg(fn, "acc", acc, "f32", main_kv.rows),
-            _arg(fn, "weights", weights, "f32", Q * k), B, Q, wp, wn)
+            _rows_out(fn, "weights", weights, "f32", Q, k), B, Q, wp, wn)
     where = seq_row_off.pages if paged else seq_row_off
     tensors = (q, seq_len, q_off, n_accept, topk, lse, acc, weights, ws, where, *_cache_tensors(main_kv))
     if paged:
@@ -648,7 +656,7 @@ def csa2_cache_evict(main_src, idx_src, acc_src, src, seq_len, keep, max_len, ma
     n_dst = main_dst.rows if idx_dst is None else min(main_dst.rows, idx_dst.rows)
     ac, sl, kp = (_arg(fn, "acc_src", acc_src, "f32", n_src), _arg(fn, "seq_len", seq_len, "i32", B),
                   _arg(fn, "keep", keep, "i32", B))
-    ad, ko, so = (_arg(fn, "acc_dst", acc_dst, "f32", n_dst), _arg(fn, "kept", kept, "i32", B * max_keep),
+    ad, ko, so = (_arg(fn, "acc_dst", acc_dst, "f32", n_dst), _rows_out(fn, "kept", kept, "i32", B, max_keep),
                   _arg(fn, "seq_len_out", seq_len_out, "i32", B))
     tensors = (acc_src, seq_len, keep, acc_dst, kept, seq_len_out, ws, src.pages if paged else src,
                dst.pages if paged else dst, *_cache_tensors(main_src, idx_src, main_dst, idx_dst))
@@ -686,7 +694,7 @@ def csa2_cache_evict_layers(main_src, idx_src, acc_src, src, seq_len, keep, max_
     head = (n, caches(main_src), caches(idx_src), accs("acc_src", acc_src, n_src))
     there = (caches(main_dst), caches(idx_dst), accs("acc_dst", acc_dst, n_dst))
     sl, kp = _arg(fn, "seq_len", seq_len, "i32", B), _arg(fn, "keep", keep, "i32", B)
-    tail = (_arg(fn, "kept", kept, "i32", B * max_keep), _arg(fn, "seq_len_out", seq_len_out, "i32", B), B,
+    tail = (_rows_out(fn, "kept", kept, "i32", B, max_keep), _arg(fn, "seq_len_out", seq_len_out, "i32", B), B,
             int(max_len), int(max_keep), int(first), int(last), wp, wn)
     tensors = (*acc_src, seq_len, keep, *acc_dst, kept, seq_len_out, ws, src.pages if paged else src,
                dst.pages if paged else dst, *_cache_tensors(*main_src, *idx_src, *main_dst, *idx_dst))

@@ -260,3 +260,37 @@ def test_evict_sets_one_shared_memory_limit_for_all_sizes(tmp_path):
     assert len({v for _, v in sizes}) > 3 and len({f for f, _ in sizes}) == 2     # one layer, and several
     assert all(len(v) == 1 for v in limits.values()), limits
     assert all(v <= max(limits[f]) for f, v in sizes)
+
+
+# ---------------------------------------------------------------------------
+# outputs whose rows lie apart
+# ---------------------------------------------------------------------------
+
+def test_outputs_with_other_row_lengths_are_refused(fake):  # noqa: F811
+    """The library writes rows of max_keep (or k) elements: in a wider buffer every row but the first would lie elsewhere
+    than its index says.  A flat buffer holds the rows one behind the other."""
+    src, dst = _full_cache(), _full_cache()
+    off, ws = torch.zeros(2, dtype=torch.int64), _z(256)
+    one = lambda kept: C.csa2_cache_evict(  # noqa: E731
+        src.main, src.idx, src.acc, off, _i(2), _i(2), 32, 16, dst.main, dst.idx, dst.acc, off, kept, _i(2), ws)
+    many = lambda kept: C.csa2_cache_evict_layers(  # noqa: E731
+        [src.main] * 2, None, [src.acc] * 2, off, _i(2), _i(2), 32, 16, [dst.main] * 2, None, [dst.acc] * 2, off, kept,
+        _i(2), ws)
+    for call in (one, many):
+        for bad in (_i(2, 17), _i(2, 20), _i(1, 32), _i(4, 8), _i(2, 1, 16), _i(31), [0] * 32):
+            with pytest.raises(C.Csa2Error, match="kept"):
+                call(bad)
+        assert not fake.calls
+        for good in (_i(2, 16), _i(3, 16), _i(32), _i(40)):
+            call(good)
+        assert len(fake.calls) == 4
+        fake.calls.clear()
+    weights = lambda w: C.csa2_attn_weights(  # noqa: E731
+        torch.zeros((2, 16, 512), dtype=torch.bfloat16), src.main, off, _i(2), _i(2, 8), torch.zeros((2, 16)), 0.1, src.acc,
+        ws, weights=w)
+    for bad in (torch.zeros((2, 9)), torch.zeros((1, 16)), torch.zeros((4, 4)), torch.zeros(15)):
+        with pytest.raises(C.Csa2Error, match="weights"):
+            weights(bad)
+    assert not fake.calls
+    for good in (torch.zeros((2, 8)), torch.zeros((5, 8)), torch.zeros(16), None):
+        weights(good)
