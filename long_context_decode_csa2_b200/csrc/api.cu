@@ -584,7 +584,7 @@ csa2_status csa2_index_prefill(csa2_mxfp4_cache idx_k, const uint8_t* q_codes, c
   if (pool_blocks < k)
     return fail(CSA2_ERR_UNSUPPORTED, std::string(fn) + ": prefill needs pool_blocks >= k");
   if (T == 0) return CSA2_OK;
-  if (!cache_ok(idx_k) || (row0 % 8) != 0 || row0 + n_entries > idx_k.rows || n_entries > INT32_MAX)
+  if (!cache_ok(idx_k) || (row0 % 8) != 0 || n_entries > INT32_MAX || row0 > idx_k.rows - n_entries)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad cache, row0 or n_entries");
   if (!q_codes || !q_scales || !w || !q_pos || !pool_out || !topk_out || !workspace)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");
@@ -776,7 +776,7 @@ csa2_status csa2_sparse_attn_prefill(const uint16_t* q, const int32_t* q_pos, in
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad size");
   if (ratio != 1 && ratio != 2) return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": ratio must be 1 or 2");
   if (T == 0) return CSA2_OK;
-  if (!cache_ok(main_kv) || row0 + n_entries > main_kv.rows || n_entries > INT32_MAX)
+  if (!cache_ok(main_kv) || n_entries > INT32_MAX || row0 > main_kv.rows - n_entries)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": bad cache, row0 or n_entries");
   if (!q || !q_pos || !topk || !raw_win || !out || !workspace)
     return fail(CSA2_ERR_INVALID_ARG, std::string(fn) + ": null pointer");

@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t seg_len_checked(const SegDesc& sd, int s, uin
     return L;
   }
   const int64_t off = sd.row_off ? sd.row_off[s] : sd.row0;
-  if ((off & 7) != 0 || off < 0 || off + L > sd.cache_rows) {
+  if ((off & 7) != 0 || off < 0 || off > sd.cache_rows - L) {
     set_status(status, CSA2_DEV_ROW_LAYOUT);
     L = 0;
   }

@@ -84,7 +84,7 @@ __device__ __forceinline__ Plan make_plan(const EvictArgs& a, int b, uint32_t* s
     n = a.max_keep;
   }
   const bool fits = a.dst_pages ? n <= (int64_t(a.dst_max_pages) << a.dst_shift)
-                                : dst_off >= 0 && (dst_off & 7) == 0 && dst_off + n <= a.dst_rows;
+                                : dst_off >= 0 && (dst_off & 7) == 0 && dst_off <= a.dst_rows - n;
   if (!fits) {
     set_status(status, CSA2_DEV_ROW_LAYOUT);
     n = 0;

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(1024) k_multi_prep(const int64_t* seq_row_off,
           set_status(status, CSA2_DEV_LENGTH);
           v = max_vis;
         }
-        if ((off & 7) != 0 || off < 0 || off + v > cache_rows) {
+        if ((off & 7) != 0 || off < 0 || off > cache_rows - v) {
           set_status(status, CSA2_DEV_ROW_LAYOUT);
           v = 0;
         }

@@ -294,3 +294,24 @@ def test_outputs_with_other_row_lengths_are_refused(fake):  # noqa: F811
     assert not fake.calls
     for good in (torch.zeros((2, 8)), torch.zeros((5, 8)), torch.zeros(16), None):
         weights(good)
+
+
+# ---------------------------------------------------------------------------
+# offsets near the end of 64 bits
+# ---------------------------------------------------------------------------
+
+def test_prefill_refuses_rows_whose_sum_wraps():
+    """A row offset so large that its sum with the length is negative lies outside the cache like any other."""
+    L, at, cache = C.lib(), GIB, C.MXFP4Cache(GIB, GIB, 4096)
+
+    def index(row0, n=1024):
+        return L.csa2_index_prefill(cache, at, at, at, at, 4, row0, n, 1, 64, 64, at, at, at, 255, None)
+
+    def attend(row0, n=1024):
+        return L.csa2_sparse_attn_prefill(at, at, 4, cache, row0, n, 1, at, 64, at, 100, 1.0, 0.1, at, None, at, 255, None)
+
+    for call in (index, attend):
+        assert call(0) == call(3072) == -3                  # sound but for the workspace
+        for row0 in (3080, 2 ** 31 - 8, 2 ** 63 - 8, 2 ** 63 - 1024):
+            assert call(row0) == -1
+        assert call(0, 2 ** 31) == -1 and call(0, 4104) == -1

@@ -473,3 +473,37 @@ def test_select_by_pairs_of_ctas_gives_what_one_gives(lens):
     for pool, top in got[1:]:
         assert torch.equal(pool, got[0][0]) and torch.equal(top, got[0][1])
     assert [(r >= 0).sum().item() for r in got[0][1]] == [min(k, n) for n in lens]
+
+
+# ---------------------------------------------------------------------------
+# offsets near the end of 64 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("far", [2 ** 63 - 8, 2 ** 63 - 512, 2 ** 40])
+def test_offsets_whose_sum_wraps_are_outside(far):
+    """A row offset so large that its sum with the length is negative: the sequence is left out and flagged."""
+    c = EvictCase([300, 700], "mixed", seed=1)
+    good = c.call([100, 200], 200)
+    for side in ("off", "doff"):
+        keep, at = getattr(c, side), getattr(c, side).copy()
+        at[0] = far
+        setattr(c, side, at)
+        got = c.call([100, 200], 200)
+        assert got["flags"] == 2 and host(got["len"]).tolist() == [0, 200]
+        assert torch.equal(got["kept"][1], good["kept"][1]) and (got["kept"][0] == -1).all()
+        setattr(c, side, keep)
+    w = WeightCase([300, 700], [2, 2], 64, seed=2)
+    full, w.off = w.call(), np.array([far, w.off[1]])
+    got = w.call()
+    assert got["flags"] == 3 and not host(got["w"])[:2].any() and torch.equal(got["w"][2:], full["w"][2:])
+    acc, ws = torch.ones(64, device="cuda"), C.workspace(256)
+    C.csa2_acc_clear(acc, torch.tensor([far, 32], device="cuda"), _i32([0, 0]), _i32([16, 8]), ws)
+    assert C.device_status(ws) == 2 and acc.sum() == 56 and not acc[32:40].any()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    by = lambda lo, hi, *s: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    idx = C.cache(by(0, 256, 4096, 64), by(120, 130, 4096, 4))
+    pool, top = (torch.full((2, n), -9, dtype=torch.int32, device="cuda") for n in (64, 64))
+    ws = C.workspace(C.csa2_index_full_workspace_bytes(2, 2048, 64, 64))
+    C.csa2_index_full(idx, by(0, 256, 2, 4, 64), by(120, 130, 2, 4, 4), torch.rand((2, 4), device="cuda", generator=g),
+                      torch.tensor([far, 2048], device="cuda"), _i32([1000, 1000]), 2048, 64, 64, pool, top, ws)
+    assert C.device_status(ws) == 2 and (top[0] == -1).all() and (top[1] >= 0).all()
