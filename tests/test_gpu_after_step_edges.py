@@ -236,6 +236,42 @@ def test_evict_layers_with_shared_accumulators():
         assert all(torch.equal(a, b) for a, b in zip(d[2:], c.dplanes[2:]))   # no indexer cache was given
 
 
+def test_evict_layers_captured_and_replayed():
+    """One graph of two layers' eviction on a side stream, replayed over changing accumulators and lengths."""
+    a, b = EvictCase([5000, 300], seed=1), EvictCase([5000, 300], seed=2)
+    acc = [dev(a.acc), dev(b.acc)]
+    dst = [[p.clone() for p in c.dplanes] for c in (a, b)]
+    dacc = [torch.zeros(a.drows, device="cuda") for _ in range(2)]
+    src, keep = [C.cache(*c.planes[:2]) for c in (a, b)], _i32([1000, 60])
+    at, to, mains = dev(a.off), dev(a.doff), [C.cache(*d[:2]) for d in dst]
+    seq_len, ln, kept = _i32([5000, 300]), _i32([0, 0]), torch.zeros((2, 1000), dtype=torch.int32, device="cuda")
+    ws = C.workspace(C.csa2_cache_evict_workspace_bytes(2, 5000))
+
+    def go():
+        C.csa2_cache_evict_layers(src, None, acc, at, seq_len, keep, 5000, 1000, mains, None, dacc, to, kept, ln, ws,
+                                  first=1, last=9)
+
+    go()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream, capture_error_mode="thread_local"):
+        go()
+    for turn, lens in enumerate(([5000, 300], [4097, 12], [9, 300])):
+        g = torch.Generator(device="cuda").manual_seed(turn)
+        seq_len.copy_(_i32(lens))
+        for x in acc:
+            x.copy_(torch.rand(len(x), device="cuda", generator=g))
+        graph.replay()
+        total = host(acc[0]) + host(acc[1])
+        for s, L in enumerate(lens):
+            pos = R.evict_positions(total[a.row_of(s, np.arange(L))], [1000, 60][s], 1, 9)
+            assert host(ln)[s] == len(pos) and np.array_equal(host(kept)[s, :len(pos)], pos)
+            for c, d, x, y in zip((a, b), dst, acc, dacc):
+                rows, there = torch.from_numpy(a.row_of(s, pos)).cuda(), torch.from_numpy(a.drow_of(s, np.arange(len(pos)))).cuda()
+                assert torch.equal(d[0][there], c.planes[0][rows]) and torch.equal(y[there], x[rows])
+    assert C.device_status(ws) == 0
+
+
 @pytest.mark.parametrize("page", [0, 512])
 def test_decode_after_eviction_of_two_full_layers(page):
     """FRUFR: the second Full layer selects inside the first one's pool on its own caches.  Its accumulators differ from
