@@ -98,7 +98,7 @@ __device__ __forceinline__ Plan make_plan(const EvictArgs& a, int b, uint32_t* s
 
 // Inclusive sum over the lanes up to this one (the shuffle's own predicate says
 // whether there is a lane d below).
-__device__ __forceinline__ uint32_t warp_incl(uint32_t v, int) {
+__device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1)
     asm volatile(
@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, L layer
     // thread t owns (2047 - 2t and 2046 - 2t); zeroes the histogram.
     auto find = [&](const uint32_t* counts, int shift, uint32_t width) {
       const uint32_t v0 = counts[kBins - 1 - 2 * tid], v1 = counts[kBins - 2 - 2 * tid];
-      const uint32_t incl = warp_incl(v0 + v1, lane);
+      const uint32_t incl = warp_incl(v0 + v1);
       if (lane == 31) sm.scan[warp] = incl;
       sm.hist[kBins - 1 - 2 * tid] = sm.hist[kBins - 2 - 2 * tid] = 0;
       __syncthreads();
-      const uint32_t part = warp_incl(sm.scan[lane], lane);
+      const uint32_t part = warp_incl(sm.scan[lane]);
       uint32_t prior = __shfl_sync(0xffffffffu, part, (warp + 31) & 31);
       prior = (warp ? prior : 0u) + incl - v0 - v1;
       if (prior < left && prior + v0 + v1 >= left) {
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kEThreads) k_evict_select(EvictArgs a, L layer
     }
     const uint32_t flags = (stays[0] ? 1u : 0u) + (stays[1] ? 1u << 8 : 0u) + (stays[2] ? 1u << 16 : 0u) +
                            (stays[3] ? 1u << 24 : 0u);
-    const uint32_t incl = warp_incl(flags, lane), sum = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t incl = warp_incl(flags), sum = __shfl_sync(0xffffffffu, incl, 31);
     // four indexes from `at` (each below 128): entries of earlier groups of 32, and of lanes below
     const uint32_t idx = incl - flags + sum * 0x01010100u;
     int32_t* to = kept + at;

@@ -50,9 +50,9 @@ constexpr uint32_t kBig = 224;                // scale bytes from here on take t
 
 // kTiles: MMA tiles (16 rows) of a warp's group.  Two tiles halve the shared
 // memory reads of the query, which bound the kernel next to the instructions
-// (48 sequences of up to 16 candidates, k = 2048: 97.6 us with one tile, 85.8
+// (48 sequences of up to 16 candidates, k = 2048: 94.1 us with one tile, 80.6
 // with two); one tile spreads few rows over more warps (64 queries of k = 512:
-// 8.5 against 9.5 us).
+// 7.5 against 9.5 us).
 template <int kTiles>
 struct Cfg {
   static constexpr int kWarps = 4;                   // per CTA; they share the query
