@@ -278,6 +278,8 @@ class DecodeStep:
         is not used."""
         if (self.queries is None) != (q_off is None and q_vis is None):
             raise ValueError("q_off / q_vis go with (and only with) a verification step")
+        if self.queries is not None and not isinstance(seq_row_off, torch.Tensor):
+            raise ValueError("a verification step takes row offsets (its scan, csa2_index_multi, has no paged form)")
         main = stream if stream is not None else torch.cuda.current_stream()
         if self.ratio == 2:
             if new_tokens is None or len(new_tokens) != len(self.pairs):

@@ -315,3 +315,10 @@ def test_prefill_refuses_rows_whose_sum_wraps():
         for row0 in (3080, 2 ** 31 - 8, 2 ** 63 - 8, 2 ** 63 - 1024):
             assert call(row0) == -1
         assert call(0, 2 ** 31) == -1 and call(0, 4104) == -1
+
+
+def test_verification_steps_take_row_offsets(fake):  # noqa: F811
+    step = DecodeStep("FU", 2, 32, 16, 8, device="cpu", concurrent=False, queries=5)
+    with pytest.raises(ValueError, match="row offsets"):
+        step.run([_full_cache()], C.PageTable(_i(2, 1), 512), _i(2), [{}, {}], q_off=_i(3), q_vis=_i(5))
+    assert not fake.calls
